@@ -311,6 +311,58 @@ int bd_attn_bwd_noalloc(const void* dout, const void* q, const void* k, const vo
                         const float* lse, const void* seg, const bd_geom* g, int grad_dtype, void* dq, void* dk,
                         void* dv, int32_t* status, bd_stream_t stream);
 
+/* ---- attention sinks ------------------------------------------------------
+ *
+ * A sliding window in which the first n_sink tokens of every document stay
+ * visible: a real row at global position p of a document that starts at d sees
+ * its key s <= p iff p - s < window or s - d < n_sink. n_sink is 0 to
+ * BD_SINK_MAX; without a window (window <= 0) every earlier key of the document
+ * is visible already and n_sink has no effect. Every head dim, layout, chunking
+ * and dropout of the entry points above.
+ *
+ * The table: as bd_attn_seg_build (kv_chunk = 0; the K/V buffer must hold
+ * [s_first, real_end): the sinks of the straddling document are needed) or
+ * bd_attn_seg_build_chunk (kv_chunk = 1), with the backward's work behind it:
+ * bd_attn_sink_seg_bytes bytes, 16-byte aligned. Its first bd_attn_seg_bytes
+ * bytes are laid out as an ordinary table, with qt_krange the K/V tiles of the
+ * window and kt_qrange covering the rows that reach a tile through its sinks
+ * too. A table belongs to the n_sink it was built for: the kernels set
+ * BD_STATUS_BOUNDS for another one's (ordinary entry points take only n_sink 0).
+ *
+ * As in the other entry points, every q, k, v and dout row must hold finite
+ * values, masked or not (a masked weight is a zero that is multiplied). */
+#define BD_SINK_MAX 128
+size_t bd_attn_sink_seg_bytes(const bd_geom* g, int n_sink);
+int bd_attn_sink_seg_build(const int32_t* doc_ids, const bd_geom* g, int n_sink, int kv_chunk, void* seg,
+                           int32_t* status, bd_stream_t stream);
+
+/* Forward, and the forward over a K/V chunk merged into a running result:
+ * bd_attn_fwd and bd_attn_fwd_merge with the sinks visible. */
+int bd_attn_sink_fwd(const void* q, const void* k, const void* v, const void* seg, const bd_geom* g, int n_sink,
+                     void* out, float* lse, int32_t* status, bd_stream_t stream);
+int bd_attn_sink_fwd_merge(const void* q, const void* k, const void* v, const void* seg, const bd_geom* g, int n_sink,
+                           void* out, float* lse, int32_t* status, bd_stream_t stream);
+
+/* Backward: bd_attn_bwd and bd_attn_bwd_deterministic with the sinks visible.
+ * A sink's dk / dv sums over all later rows of its document; those rows are cut
+ * into units that run side by side, each leaves its fp32 share in the
+ * workspace, and a last kernel adds them in a fixed order and rounds once.
+ * workspace: bd_attn_sink_bwd_workspace_bytes bytes, 256-byte aligned. For K/V
+ * chunks: bd_attn_bwd_prep once, bd_attn_sink_bwd_main per chunk (with that
+ * chunk's table, kv_chunk = 1), then bd_attn_bwd_finalize, all with one
+ * workspace of the largest chunk's size. */
+size_t bd_attn_sink_bwd_workspace_bytes(const bd_geom* g, int n_sink);
+int bd_attn_sink_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out, const float* lse,
+                     const void* seg, const bd_geom* g, int n_sink, int grad_dtype, void* dq, void* dk, void* dv,
+                     void* workspace, int32_t* status, bd_stream_t stream);
+int bd_attn_sink_bwd_deterministic(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                                   const float* lse, const void* seg, const bd_geom* g, int n_sink, int grad_dtype,
+                                   void* dq, void* dk, void* dv, void* workspace, int32_t* status,
+                                   bd_stream_t stream);
+int bd_attn_sink_bwd_main(const void* dout, const void* q, const void* k, const void* v, const float* lse,
+                          const void* seg, const bd_geom* g, int n_sink, int grad_dtype, void* dk, void* dv,
+                          void* workspace, int32_t* status, bd_stream_t stream);
+
 /* ---- K/V exchange plans (blockdiag_cp.exchange) --------------------------
  *
  * The global left-halo plan and the needed-only all-to-all-v split plan,

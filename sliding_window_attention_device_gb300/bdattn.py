@@ -8,6 +8,7 @@ library, or without a GPU, these functions raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -38,6 +39,9 @@ EXPORTS = ("bd_attn_seg_bytes", "bd_attn_seg_layout", "bd_attn_seg_build", "bd_a
            "bd_attn_bwd_finalize", "bd_attn_bwd_prep_dq", "bd_attn_bwd_main_dq",
            "bd_attn_bwd_noalloc", "bd_attn_plan_bytes", "bd_attn_plan_layout", "bd_attn_exchange_plan",
            "bd_attn_needed_gather", "bd_attn_needed_scatter_add", "bd_attn_strerror",
+           "bd_attn_sink_seg_bytes", "bd_attn_sink_seg_build", "bd_attn_sink_fwd", "bd_attn_sink_fwd_merge",
+           "bd_attn_sink_bwd_workspace_bytes", "bd_attn_sink_bwd", "bd_attn_sink_bwd_deterministic",
+           "bd_attn_sink_bwd_main",
            "bd_attn_selftest_wait_timeout")
 
 # exchange plan: header fields (BD_PLAN_*) and regions (BD_PLAN_OFF_*)
@@ -137,6 +141,17 @@ def load() -> ctypes.CDLL:
         lib.bd_attn_needed_gather.restype = I
         lib.bd_attn_needed_scatter_add.argtypes = [P, P, I, I, I, I, I, P, I, P, P]
         lib.bd_attn_needed_scatter_add.restype = I
+        for name in ("bd_attn_sink_seg_bytes", "bd_attn_sink_bwd_workspace_bytes"):
+            getattr(lib, name).argtypes = [G, I]
+            getattr(lib, name).restype = ctypes.c_size_t
+        lib.bd_attn_sink_seg_build.argtypes = [P, G, I, I, P, P, P]
+        lib.bd_attn_sink_fwd.argtypes = [P, P, P, P, G, I, P, P, P, P]
+        lib.bd_attn_sink_fwd_merge.argtypes = [P, P, P, P, G, I, P, P, P, P]
+        lib.bd_attn_sink_bwd.argtypes = [P, P, P, P, P, P, P, G, I, I, P, P, P, P, P, P]
+        lib.bd_attn_sink_bwd_deterministic.argtypes = [P, P, P, P, P, P, P, G, I, I, P, P, P, P, P, P]
+        lib.bd_attn_sink_bwd_main.argtypes = [P, P, P, P, P, P, G, I, I, P, P, P, P, P]
+        for name in ("seg_build", "fwd", "fwd_merge", "bwd", "bwd_deterministic", "bwd_main"):
+            getattr(lib, "bd_attn_sink_" + name).restype = I
         lib.bd_attn_strerror.argtypes = [ctypes.c_int]
         lib.bd_attn_strerror.restype = ctypes.c_char_p
         lib.bd_attn_selftest_wait_timeout.argtypes = [P, ctypes.c_uint64, P]
@@ -430,6 +445,160 @@ def read_seg(seg: torch.Tensor, g: Geom) -> dict:
             "bwd_work": a[lay["bwd_work"]: lay["bwd_work"] + B * nkt].copy(),
             "counts": a[lay["counts"]: lay["counts"] + 4].copy(),
             "layout": lay}
+
+
+# ------------------------------------------------------------ attention sinks
+SINK_MAX = 128  # BD_SINK_MAX
+
+
+def _on(dev, stream):
+    """Context with `dev` current and new tensors owned by the stream the call
+    runs on, and that stream. The caller's other tensors have to be ready on it."""
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if s.device != dev:
+        raise ValueError(f"the stream is on {s.device}, the tensors are on {dev}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext(), ctypes.c_void_p(s.cuda_stream)
+    return torch.cuda.stream(s), ctypes.c_void_p(s.cuda_stream)
+
+
+def _cuda_device(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def sink_seg_bytes(g: Geom, n_sink: int) -> int:
+    n = load().bd_attn_sink_seg_bytes(ctypes.byref(g), int(n_sink))
+    if n == 0:
+        raise ValueError(f"invalid geometry {g} or n_sink={n_sink} (0 to {SINK_MAX})")
+    return int(n)
+
+
+def sink_bwd_workspace_bytes(g: Geom, n_sink: int) -> int:
+    n = load().bd_attn_sink_bwd_workspace_bytes(ctypes.byref(g), int(n_sink))
+    if n == 0:
+        raise ValueError(f"invalid geometry {g} or n_sink={n_sink} (0 to {SINK_MAX})")
+    return int(n)
+
+
+def bd_attn_sink_seg_build(doc_ids: torch.Tensor, g: Geom, n_sink: int, kv_chunk: bool = False,
+                           seg: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Table of the shard with the first `n_sink` tokens of every document
+    visible past the window; `kv_chunk`: of one chunk of the K/V range. Returns
+    (seg, status); `seg` serves every bd_attn_sink_* call of this geometry and n_sink."""
+    dev = _cuda_device(doc_ids, "doc_ids")
+    _need(doc_ids, "doc_ids", torch.int32, (g.B, g.S_full), None)
+    n = sink_seg_bytes(g, n_sink) // 4
+    ctx, st = _on(dev, stream)
+    with ctx:
+        if seg is None:
+            seg = torch.empty(n, dtype=torch.int32, device=dev)
+        if status is None:
+            status = new_status(dev)
+        _need(seg, "seg", torch.int32, (n,), dev)
+        _need(status, "status", torch.int32, (1,), dev)
+        _check(load().bd_attn_sink_seg_build(_ptr(doc_ids), ctypes.byref(g), int(n_sink), int(bool(kv_chunk)),
+                                             _ptr(seg), _ptr(status), st), "bd_attn_sink_seg_build")
+    return seg, status
+
+
+def bd_attn_sink_fwd(q, k, v, seg, g: Geom, n_sink: int, status, out=None, lse=None, stream=None,
+                     _fn="bd_attn_sink_fwd"):
+    """bd_attn_fwd with the documents' first n_sink tokens visible past the window."""
+    dev = _cuda_device(q, "q")
+    _need(q, "q", torch.bfloat16, (g.B, g.Hq, g.L, g.D), dev)
+    _need(k, "k", torch.bfloat16, kv_shape(g), dev)
+    _need(v, "v", torch.bfloat16, kv_shape(g), dev)
+    _need(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
+    _need(status, "status", torch.int32, (1,), dev)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(g.B, g.Hq, g.L, g.D, dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty(g.B, g.Hq, g.L, dtype=torch.float32, device=dev)
+        _need(out, "out", torch.bfloat16, (g.B, g.Hq, g.L, g.D), dev)
+        _need(lse, "lse", torch.float32, (g.B, g.Hq, g.L), dev)
+        _check(getattr(load(), _fn)(_ptr(q), _ptr(k), _ptr(v), _ptr(seg), ctypes.byref(g), int(n_sink), _ptr(out),
+                                    _ptr(lse), _ptr(status), st), _fn)
+    return out, lse
+
+
+def bd_attn_sink_fwd_merge(q, k, v, seg, g: Geom, n_sink: int, status, out, lse, stream=None):
+    """bd_attn_sink_fwd over one K/V chunk merged into the running (out, lse), in place."""
+    if out is None or lse is None:
+        raise ValueError("out and lse hold the running result")
+    return bd_attn_sink_fwd(q, k, v, seg, g, n_sink, status, out, lse, stream, _fn="bd_attn_sink_fwd_merge")
+
+
+def bd_attn_sink_bwd(dout, q, k, v, out, lse, seg, g: Geom, n_sink: int, status, grad_dtype=torch.float32, dq=None,
+                     dk=None, dv=None, workspace=None, stream=None, _fn="bd_attn_sink_bwd"):
+    """Gradients of bd_attn_sink_fwd: dq [B,Hq,L,D], dk / dv in k's layout (summed over each GQA group)."""
+    dev = _cuda_device(q, "q")
+    if grad_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("grad_dtype must be torch.float32 or torch.bfloat16")
+    for name, t in (("dout", dout), ("q", q), ("out", out)):
+        _need(t, name, torch.bfloat16, (g.B, g.Hq, g.L, g.D), dev)
+    _need(k, "k", torch.bfloat16, kv_shape(g), dev)
+    _need(v, "v", torch.bfloat16, kv_shape(g), dev)
+    _need(lse, "lse", torch.float32, (g.B, g.Hq, g.L), dev)
+    _need(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
+    _need(status, "status", torch.int32, (1,), dev)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        if dq is None:
+            dq = torch.empty(g.B, g.Hq, g.L, g.D, dtype=grad_dtype, device=dev)
+        if dk is None:
+            dk = torch.empty(kv_shape(g), dtype=grad_dtype, device=dev)
+        if dv is None:
+            dv = torch.empty(kv_shape(g), dtype=grad_dtype, device=dev)
+        if workspace is None:
+            workspace = torch.empty(sink_bwd_workspace_bytes(g, n_sink), dtype=torch.uint8, device=dev)
+        _need(dq, "dq", grad_dtype, (g.B, g.Hq, g.L, g.D), dev)
+        _need(dk, "dk", grad_dtype, kv_shape(g), dev)
+        _need(dv, "dv", grad_dtype, kv_shape(g), dev)
+        _need(workspace, "workspace", torch.uint8, (sink_bwd_workspace_bytes(g, n_sink),), dev)
+        code = BD_DTYPE_BF16 if grad_dtype == torch.bfloat16 else BD_DTYPE_F32
+        _check(getattr(load(), _fn)(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(seg),
+                                    ctypes.byref(g), int(n_sink), code, _ptr(dq), _ptr(dk), _ptr(dv),
+                                    _ptr(workspace), _ptr(status), st), _fn)
+    return dq, dk, dv
+
+
+def bd_attn_sink_bwd_deterministic(dout, q, k, v, out, lse, seg, g: Geom, n_sink: int, status,
+                                   grad_dtype=torch.float32, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """bd_attn_sink_bwd with bitwise reproducible results (dq by a fixed-order pass)."""
+    return bd_attn_sink_bwd(dout, q, k, v, out, lse, seg, g, n_sink, status, grad_dtype, dq, dk, dv, workspace,
+                            stream, _fn="bd_attn_sink_bwd_deterministic")
+
+
+def bd_attn_sink_bwd_main(dout, q, k, v, lse, seg, g: Geom, n_sink: int, status, workspace, dk, dv, stream=None):
+    """bd_attn_bwd_main with sinks, for K/V chunks: dk, dv (dtype of dk) of the chunk and its dq share, between
+    bd_attn_bwd_prep and bd_attn_bwd_finalize. `workspace`: uint8, at least sink_bwd_workspace_bytes of every
+    chunk; the other two stages take its first bwd_workspace_bytes(g) bytes."""
+    dev = _cuda_device(q, "q")
+    gd = dk.dtype
+    if gd not in (torch.float32, torch.bfloat16):
+        raise ValueError("dk / dv must be float32 or bfloat16")
+    for name, t in (("dout", dout), ("q", q)):
+        _need(t, name, torch.bfloat16, (g.B, g.Hq, g.L, g.D), dev)
+    _need(k, "k", torch.bfloat16, kv_shape(g), dev)
+    _need(v, "v", torch.bfloat16, kv_shape(g), dev)
+    _need(lse, "lse", torch.float32, (g.B, g.Hq, g.L), dev)
+    _need(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
+    _need(dk, "dk", gd, kv_shape(g), dev)
+    _need(dv, "dv", gd, kv_shape(g), dev)
+    _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    if workspace.numel() < sink_bwd_workspace_bytes(g, n_sink):
+        raise ValueError(f"workspace: {workspace.numel()} bytes, {sink_bwd_workspace_bytes(g, n_sink)} needed")
+    _need(status, "status", torch.int32, (1,), dev)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        code = BD_DTYPE_BF16 if gd == torch.bfloat16 else BD_DTYPE_F32
+        _check(load().bd_attn_sink_bwd_main(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(lse), _ptr(seg),
+                                            ctypes.byref(g), int(n_sink), code, _ptr(dk), _ptr(dv), _ptr(workspace),
+                                            _ptr(status), st), "bd_attn_sink_bwd_main")
 
 
 # ------------------------------------------------------------ exchange plans

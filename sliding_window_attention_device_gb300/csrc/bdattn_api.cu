@@ -44,6 +44,8 @@ cudaError_t launch_needed_gather(const void* x, const int32_t* plan, int B, int 
 cudaError_t launch_needed_scatter_add(const void* gsend, const int32_t* plan, int B, int C, int L, int vshift,
                                       int bf16, void* glocal, int max_rows, int32_t* status, cudaStream_t st);
 int bwd_q_box_rows(int D);
+cudaError_t launch_sink_sum(const int32_t* seg, const Geom& g, void* dk, void* dv, int bf16, int32_t* status,
+                            cudaStream_t st);
 
 __global__ void selftest_wait_kernel(int32_t* status, uint64_t limit_ns) {
   __shared__ uint64_t bar;
@@ -124,7 +126,28 @@ int to_geom(const bd_geom* in, Geom* g) {
   g->scale = in->scale > 0.f ? in->scale : 1.0f / std::sqrt(static_cast<float>(in->D));
   g->kv_tm = in->kv_layout == BD_KV_SBHD;
   seg_layout(g->B, g->L, g->S_kv, g->off, &g->nqt, &g->nkt, &g->nkw);
+  g->n_sink = 0;
+  g->sink_tab = 0;
+  g->sk_off = g->sk_units = g->sk_sums = g->sk_slots = g->sk_rows = g->sk_split = 0;
+  g->sk_part = nullptr;
   return BD_OK;
+}
+
+// The geometry with sink tokens: a table with the sink regions behind it.
+int to_geom_sink(const bd_geom* in, int n_sink, Geom* g) {
+  if (int rc = to_geom(in, g)) return rc;
+  if (n_sink < 0 || n_sink > BD_SINK_MAX) return BD_ERR_ARG;
+  g->n_sink = g->window > 0 ? n_sink : 0;  // without a window every earlier key is visible anyway
+  g->sink_tab = 1;
+  sink_sizes(g);
+  g->sk_off = align4(g->off[BD_SEG_OFF_TOTAL]);
+  if (g->sk_off + sink_words(*g) > 0x7fffffffLL) return BD_ERR_ARG;
+  return BD_OK;
+}
+
+// Bytes of the partial slots: [slots][Hkv][dk, dv][sk_rows][D] fp32.
+size_t sink_part_bytes(const Geom& g) {
+  return static_cast<size_t>(g.sk_slots) * g.Hkv * 2 * g.sk_rows * g.D * 4;
 }
 
 // 3-D bf16 map over [planes][rows][D] with a (64 x box_rows x 1) box, 128B swizzle;
@@ -244,6 +267,23 @@ int bd_attn_merge(void* out, float* lse, const void* out_chunk, const float* lse
   return cuda_rc(launch_merge(g, out, lse, out_chunk, lse_chunk, status, static_cast<cudaStream_t>(stream)));
 }
 
+size_t bd_attn_sink_seg_bytes(const bd_geom* gi, int n_sink) {
+  Geom g;
+  if (to_geom_sink(gi, n_sink, &g) != BD_OK) return 0;
+  return static_cast<size_t>(g.sk_off + sink_words(g)) * 4;
+}
+
+int bd_attn_sink_seg_build(const int32_t* doc_ids, const bd_geom* gi, int n_sink, int kv_chunk, void* seg,
+                           int32_t* status, bd_stream_t stream) {
+  Geom g;
+  if (int rc = to_geom_sink(gi, n_sink, &g)) return rc;
+  if (kv_chunk != 0 && kv_chunk != 1) return BD_ERR_ARG;
+  if (!doc_ids || !seg || !status || !aligned16(seg)) return BD_ERR_ARG;
+  if (int rc = check_device()) return rc;
+  return cuda_rc(
+      launch_seg_build(doc_ids, g, static_cast<int32_t*>(seg), status, static_cast<cudaStream_t>(stream), kv_chunk));
+}
+
 size_t bd_attn_plan_bytes(int B, int cp_size, int L) {
   int off[BD_PLAN_NOFF];
   const long long words = plan_layout(B, cp_size, L, off);
@@ -291,10 +331,11 @@ int bd_attn_needed_scatter_add(const void* grad_send, const void* plan, int B, i
 }
 
 namespace {
-int fwd_impl(const void* q, const void* k, const void* v, const void* seg, const bd_geom* gi, void* out, float* lse,
-             int32_t* status, int merge, bd_stream_t stream) {
+// n_sink < 0: an ordinary table
+int fwd_impl(const void* q, const void* k, const void* v, const void* seg, const bd_geom* gi, int n_sink, void* out,
+             float* lse, int32_t* status, int merge, bd_stream_t stream) {
   Geom g;
-  if (int rc = to_geom(gi, &g)) return rc;
+  if (int rc = n_sink < 0 ? to_geom(gi, &g) : to_geom_sink(gi, n_sink, &g)) return rc;
   if (!q || !k || !v || !seg || !out || !lse || !status) return BD_ERR_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(seg)) return BD_ERR_ARG;
   if (int rc = check_device()) return rc;
@@ -313,17 +354,34 @@ int fwd_impl(const void* q, const void* k, const void* v, const void* seg, const
 
 int bd_attn_fwd(const void* q, const void* k, const void* v, const void* seg, const bd_geom* gi, void* out,
                 float* lse, int32_t* status, bd_stream_t stream) {
-  return fwd_impl(q, k, v, seg, gi, out, lse, status, 0, stream);
+  return fwd_impl(q, k, v, seg, gi, -1, out, lse, status, 0, stream);
 }
 
 int bd_attn_fwd_merge(const void* q, const void* k, const void* v, const void* seg, const bd_geom* gi, void* out,
                       float* lse, int32_t* status, bd_stream_t stream) {
-  return fwd_impl(q, k, v, seg, gi, out, lse, status, 1, stream);
+  return fwd_impl(q, k, v, seg, gi, -1, out, lse, status, 1, stream);
+}
+
+int bd_attn_sink_fwd(const void* q, const void* k, const void* v, const void* seg, const bd_geom* gi, int n_sink,
+                     void* out, float* lse, int32_t* status, bd_stream_t stream) {
+  if (n_sink < 0) return BD_ERR_ARG;
+  return fwd_impl(q, k, v, seg, gi, n_sink, out, lse, status, 0, stream);
+}
+
+int bd_attn_sink_fwd_merge(const void* q, const void* k, const void* v, const void* seg, const bd_geom* gi,
+                           int n_sink, void* out, float* lse, int32_t* status, bd_stream_t stream) {
+  if (n_sink < 0) return BD_ERR_ARG;
+  return fwd_impl(q, k, v, seg, gi, n_sink, out, lse, status, 1, stream);
 }
 
 }  // extern "C"
 
 namespace {
+// The partial slots follow the ordinary workspace (a multiple of 256 bytes).
+void set_sink_part(Geom* g, void* workspace) {
+  g->sk_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + bwd_workspace_bytes(*g));
+}
+
 // The prep and main stages with the dq accumulator either in the workspace
 // (dq_f32 == nullptr) or in the caller's fp32 dq buffer.
 int bwd_prep_impl(const void* dout, const void* out, const bd_geom* gi, void* workspace, float* dq_f32,
@@ -338,10 +396,10 @@ int bwd_prep_impl(const void* dout, const void* out, const bd_geom* gi, void* wo
 }
 
 int bwd_main_impl(const void* dout, const void* q, const void* k, const void* v, const float* lse, const void* seg,
-                  const bd_geom* gi, int grad_dtype, void* dk, void* dv, void* workspace, float* dq_f32,
+                  const bd_geom* gi, int n_sink, int grad_dtype, void* dk, void* dv, void* workspace, float* dq_f32,
                   int32_t* status, bd_stream_t stream) {
   Geom g;
-  if (int rc = to_geom(gi, &g)) return rc;
+  if (int rc = n_sink < 0 ? to_geom(gi, &g) : to_geom_sink(gi, n_sink, &g)) return rc;
   if (!dout || !q || !k || !v || !lse || !seg || !dk || !dv || !workspace || !status) return BD_ERR_ARG;
   if (grad_dtype != BD_DTYPE_F32 && grad_dtype != BD_DTYPE_BF16) return BD_ERR_ARG;
   if (!aligned16(dout) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dk) || !aligned16(dv) ||
@@ -356,9 +414,13 @@ int bwd_main_impl(const void* dout, const void* q, const void* k, const void* v,
       make_map_kv(&mk, k, g, kTile) || make_map_kv(&mv, v, g, kTile) ||
       make_map_f32(&mdq, workspace, g.D, g.L, g.B * g.Hq))
     return BD_ERR_CUDA;
-  return cuda_rc(launch_bwd_main(mq, mdo, mk, mv, mdq, static_cast<const int32_t*>(seg), g, lse, dk, dv,
-                                 grad_dtype == BD_DTYPE_BF16, workspace, dq_f32, status,
-                                 static_cast<cudaStream_t>(stream)));
+  const int32_t* sg = static_cast<const int32_t*>(seg);
+  const int bf16 = grad_dtype == BD_DTYPE_BF16;
+  const auto st = static_cast<cudaStream_t>(stream);
+  if (g.sink_tab) set_sink_part(&g, workspace);
+  if (int rc = cuda_rc(launch_bwd_main(mq, mdo, mk, mv, mdq, sg, g, lse, dk, dv, bf16, workspace, dq_f32, status, st)))
+    return rc;
+  return g.sink_tab ? cuda_rc(launch_sink_sum(sg, g, dk, dv, bf16, status, st)) : BD_OK;
 }
 }  // namespace
 
@@ -372,7 +434,7 @@ int bd_attn_bwd_prep(const void* dout, const void* out, const bd_geom* gi, void*
 int bd_attn_bwd_main(const void* dout, const void* q, const void* k, const void* v, const float* lse,
                      const void* seg, const bd_geom* gi, int grad_dtype, void* dk, void* dv, void* workspace,
                      int32_t* status, bd_stream_t stream) {
-  return bwd_main_impl(dout, q, k, v, lse, seg, gi, grad_dtype, dk, dv, workspace, nullptr, status, stream);
+  return bwd_main_impl(dout, q, k, v, lse, seg, gi, -1, grad_dtype, dk, dv, workspace, nullptr, status, stream);
 }
 
 int bd_attn_bwd_prep_dq(const void* dout, const void* out, const bd_geom* gi, void* workspace, float* dq,
@@ -385,7 +447,7 @@ int bd_attn_bwd_main_dq(const void* dout, const void* q, const void* k, const vo
                         const void* seg, const bd_geom* gi, int grad_dtype, float* dq, void* dk, void* dv,
                         void* workspace, int32_t* status, bd_stream_t stream) {
   if (!dq) return BD_ERR_ARG;
-  return bwd_main_impl(dout, q, k, v, lse, seg, gi, grad_dtype, dk, dv, workspace, dq, status, stream);
+  return bwd_main_impl(dout, q, k, v, lse, seg, gi, -1, grad_dtype, dk, dv, workspace, dq, status, stream);
 }
 
 int bd_attn_bwd_finalize(const bd_geom* gi, int grad_dtype, void* dq, void* workspace, int32_t* status,
@@ -400,11 +462,14 @@ int bd_attn_bwd_finalize(const bd_geom* gi, int grad_dtype, void* dq, void* work
                                      static_cast<cudaStream_t>(stream)));
 }
 
-int bd_attn_bwd_deterministic(const void* dout, const void* q, const void* k, const void* v, const void* out,
-                              const float* lse, const void* seg, const bd_geom* gi, int grad_dtype, void* dq,
-                              void* dk, void* dv, void* workspace, int32_t* status, bd_stream_t stream) {
+}  // extern "C"
+
+namespace {
+int bwd_det_impl(const void* dout, const void* q, const void* k, const void* v, const void* out, const float* lse,
+                 const void* seg, const bd_geom* gi, int n_sink, int grad_dtype, void* dq, void* dk, void* dv,
+                 void* workspace, int32_t* status, bd_stream_t stream) {
   Geom g;
-  if (int rc = to_geom(gi, &g)) return rc;
+  if (int rc = n_sink < 0 ? to_geom(gi, &g) : to_geom_sink(gi, n_sink, &g)) return rc;
   if (!dout || !q || !k || !v || !out || !lse || !seg || !dq || !dk || !dv || !workspace || !status)
     return BD_ERR_ARG;
   if (grad_dtype != BD_DTYPE_F32 && grad_dtype != BD_DTYPE_BF16) return BD_ERR_ARG;
@@ -423,17 +488,20 @@ int bd_attn_bwd_deterministic(const void* dout, const void* q, const void* k, co
   const auto st = static_cast<cudaStream_t>(stream);
   const int32_t* sg = static_cast<const int32_t*>(seg);
   const int bf16 = grad_dtype == BD_DTYPE_BF16;
+  if (g.sink_tab) set_sink_part(&g, workspace);
   if (int rc = cuda_rc(launch_bwd_delta(g, dout, out, workspace, status, st))) return rc;
   if (int rc = cuda_rc(launch_bwd_main_nodq(mq_m, mdo_m, mk, mv, sg, g, lse, dk, dv, bf16, workspace, status, st)))
     return rc;
+  if (g.sink_tab)
+    if (int rc = cuda_rc(launch_sink_sum(sg, g, dk, dv, bf16, status, st))) return rc;
   return cuda_rc(launch_bwd_dq(mq, mdo, mk, mv, sg, g, lse, bwd_delta_ptr(g, workspace), dq, bf16, status, st));
 }
 
-int bd_attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out, const float* lse,
-                const void* seg, const bd_geom* gi, int grad_dtype, void* dq, void* dk, void* dv, void* workspace,
-                int32_t* status, bd_stream_t stream) {
+int bwd_impl(const void* dout, const void* q, const void* k, const void* v, const void* out, const float* lse,
+             const void* seg, const bd_geom* gi, int n_sink, int grad_dtype, void* dq, void* dk, void* dv,
+             void* workspace, int32_t* status, bd_stream_t stream) {
   Geom g;
-  if (int rc = to_geom(gi, &g)) return rc;
+  if (int rc = n_sink < 0 ? to_geom(gi, &g) : to_geom_sink(gi, n_sink, &g)) return rc;
   // check everything up front so that a bad argument enqueues nothing
   if (!dout || !q || !k || !v || !out || !lse || !seg || !dq || !dk || !dv || !workspace || !status)
     return BD_ERR_ARG;
@@ -445,12 +513,55 @@ int bd_attn_bwd(const void* dout, const void* q, const void* k, const void* v, c
     // fp32 dq is its own accumulator: no finalize pass over it
     float* dqf = static_cast<float*>(dq);
     if (int rc = bwd_prep_impl(dout, out, gi, workspace, dqf, status, stream)) return rc;
-    return bwd_main_impl(dout, q, k, v, lse, seg, gi, grad_dtype, dk, dv, workspace, dqf, status, stream);
+    return bwd_main_impl(dout, q, k, v, lse, seg, gi, n_sink, grad_dtype, dk, dv, workspace, dqf, status, stream);
   }
-  if (int rc = bd_attn_bwd_prep(dout, out, gi, workspace, status, stream)) return rc;
-  if (int rc = bd_attn_bwd_main(dout, q, k, v, lse, seg, gi, grad_dtype, dk, dv, workspace, status, stream))
+  if (int rc = bwd_prep_impl(dout, out, gi, workspace, nullptr, status, stream)) return rc;
+  if (int rc = bwd_main_impl(dout, q, k, v, lse, seg, gi, n_sink, grad_dtype, dk, dv, workspace, nullptr, status, stream))
     return rc;
   return bd_attn_bwd_finalize(gi, grad_dtype, dq, workspace, status, stream);
+}
+}  // namespace
+
+extern "C" {
+
+int bd_attn_bwd_deterministic(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                              const float* lse, const void* seg, const bd_geom* gi, int grad_dtype, void* dq,
+                              void* dk, void* dv, void* workspace, int32_t* status, bd_stream_t stream) {
+  return bwd_det_impl(dout, q, k, v, out, lse, seg, gi, -1, grad_dtype, dq, dk, dv, workspace, status, stream);
+}
+
+int bd_attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out, const float* lse,
+                const void* seg, const bd_geom* gi, int grad_dtype, void* dq, void* dk, void* dv, void* workspace,
+                int32_t* status, bd_stream_t stream) {
+  return bwd_impl(dout, q, k, v, out, lse, seg, gi, -1, grad_dtype, dq, dk, dv, workspace, status, stream);
+}
+
+size_t bd_attn_sink_bwd_workspace_bytes(const bd_geom* gi, int n_sink) {
+  Geom g;
+  if (to_geom_sink(gi, n_sink, &g) != BD_OK) return 0;
+  return bwd_workspace_bytes(g) + sink_part_bytes(g);
+}
+
+int bd_attn_sink_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out, const float* lse,
+                     const void* seg, const bd_geom* gi, int n_sink, int grad_dtype, void* dq, void* dk, void* dv,
+                     void* workspace, int32_t* status, bd_stream_t stream) {
+  if (n_sink < 0) return BD_ERR_ARG;
+  return bwd_impl(dout, q, k, v, out, lse, seg, gi, n_sink, grad_dtype, dq, dk, dv, workspace, status, stream);
+}
+
+int bd_attn_sink_bwd_deterministic(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                                   const float* lse, const void* seg, const bd_geom* gi, int n_sink, int grad_dtype,
+                                   void* dq, void* dk, void* dv, void* workspace, int32_t* status,
+                                   bd_stream_t stream) {
+  if (n_sink < 0) return BD_ERR_ARG;
+  return bwd_det_impl(dout, q, k, v, out, lse, seg, gi, n_sink, grad_dtype, dq, dk, dv, workspace, status, stream);
+}
+
+int bd_attn_sink_bwd_main(const void* dout, const void* q, const void* k, const void* v, const float* lse,
+                          const void* seg, const bd_geom* gi, int n_sink, int grad_dtype, void* dk, void* dv,
+                          void* workspace, int32_t* status, bd_stream_t stream) {
+  if (n_sink < 0) return BD_ERR_ARG;
+  return bwd_main_impl(dout, q, k, v, lse, seg, gi, n_sink, grad_dtype, dk, dv, workspace, nullptr, status, stream);
 }
 
 }  // extern "C"

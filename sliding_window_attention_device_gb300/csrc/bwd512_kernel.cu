@@ -71,6 +71,7 @@ struct Bwd512Smem {
   uint32_t tmem_base;
   int abort_flag;
   int b, kt, q64_lo, nq64, n_real, skip, work, n_att;
+  int u_flags, u_slot, u_rbase;  // kSink: the unit's flags, partial slot and first partial row
 };
 
 __device__ __forceinline__ void red_add_f32(float* addr, float v) {
@@ -81,7 +82,7 @@ __device__ __forceinline__ void red_add_f32(float* addr, float v) {
 __device__ __forceinline__ int streamed_chunk(int c, int i) { return i < 2 * c ? i : i + 2; }
 
 // kDq: with the dq products (else dK / dV only, for the fixed-order dq pass).
-template <bool kDq, bool kDrop>
+template <bool kDq, bool kDrop, bool kSink>
 __global__ void __launch_bounds__(kThreads5, 1)
     bwd512_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_dout,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -100,13 +101,15 @@ __global__ void __launch_bounds__(kThreads5, 1)
 
   if (tid == 0) {
     // the attended K/V tiles lead the work list; the grid must cover them
+    // (kSink: units, which cover the attended tiles)
     const int n_att = seg[g.off[BD_SEG_OFF_COUNTS] + 3];
+    const int n_work = kSink ? sink_n_units(g, seg) : n_att;
     int work = 0;
     s.n_att = -1;
-    if (n_att < 0 || n_att > g.B * g.nkt || n_att > static_cast<int>(gridDim.x) / (kNSlice * g.Hkv)) {
+    if (n_att < 0 || n_att > g.B * g.nkt || n_work < n_att || n_work > static_cast<int>(gridDim.x) / (kNSlice * g.Hkv)) {
       atomicOr(status, BD_STATUS_BOUNDS);
     } else {
-      work = item < n_att ? 1 : 0;
+      work = item < n_work ? 1 : 0;
       s.n_att = n_att;
     }
     s.work = work;
@@ -127,16 +130,23 @@ __global__ void __launch_bounds__(kThreads5, 1)
   }
 
   if (tid == 0) {
-    const int wi = seg[g.off[BD_SEG_OFF_BWD_WORK] + item];
+    const int32_t* u = kSink ? seg + g.sk_off + kSinkHdrWords + static_cast<size_t>(item) * kSinkUnitWords : nullptr;
+    const int wi = kSink ? u[0] : seg[g.off[BD_SEG_OFF_BWD_WORK] + item];
     int ok = wi >= 0 && wi < g.B * g.nkt;
     const int b = ok ? wi / g.nkt : 0, kt = ok ? wi % g.nkt : 0;
     const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
     ok = ok && hdr[kHdrMagic] == kSegMagic && hdr[kHdrRowOffset] == g.row_offset && hdr[kHdrL] == g.L &&
          hdr[kHdrKvOffset] == g.kv_offset && hdr[kHdrSkv] == g.S_kv && hdr[kHdrWindow] == g.window &&
-         hdr[kHdrSfull] == g.S_full;
+         hdr[kHdrSfull] == g.S_full && hdr[kHdrSink] == g.n_sink;
     const int n_real = hdr[BD_SEG_N_REAL];
     const int32_t* qr = seg + g.off[BD_SEG_OFF_KT_QRANGE] + (b * g.nkt + kt) * 2;
-    const int qlo = qr[0], qhi = qr[1];
+    const int qlo = kSink ? u[1] : qr[0], qhi = kSink ? u[2] : qr[1];
+    if constexpr (kSink) {
+      s.u_flags = u[3];
+      s.u_slot = u[4];
+      s.u_rbase = u[5];
+      ok = ok && u[4] < g.sk_slots && u[5] >= 0 && u[5] < kTile;
+    }
     // an attended tile has a non-empty q range
     ok = ok && n_real >= 0 && n_real <= g.L && qlo >= 0 && qhi <= n_real && qlo < qhi;
     if (!ok) atomicOr(status, BD_STATUS_BOUNDS);
@@ -380,7 +390,7 @@ __global__ void __launch_bounds__(kThreads5, 1)
     // attending s are [s, min(doc_end(s), s + W)) of the real rows, doc_end(s)
     // found once from cu_q.
     const int key = g.kv_offset + j;  // global position of this thread's key
-    int doc_end = -0x40000000;        // keys no local row attends
+    int doc_beg = 0, doc_end = -0x40000000;  // keys no local row attends
     {
       const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
       const int32_t* cu_q = seg + g.off[BD_SEG_OFF_CU_Q] + b * (g.L + 1);
@@ -396,9 +406,12 @@ __global__ void __launch_bounds__(kThreads5, 1)
           k = a;
         }
         doc_end = g.row_offset + cu_q[k + 1];
+        if constexpr (kSink) doc_beg = k == 0 ? hdr[BD_SEG_S_FIRST] : g.row_offset + cu_q[k];
       }
     }
-    const int row_end = min(doc_end, g.window > 0 ? key + g.window : 0x3fffffff);
+    int row_beg = key, row_end = min(doc_end, g.window > 0 ? key + g.window : 0x3fffffff);
+    if constexpr (kSink)  // in this unit
+      unit_rows(g, key, doc_beg, doc_end, (s.u_flags & kUnitSink) != 0, &row_beg, &row_end);
     // dropout: scale * keep scale multiplies a kept dP (a dropped one is zero)
     const float sc_dp = kDrop ? g.scale * g.drop_scale : g.scale;
     bool ok = true;
@@ -421,7 +434,7 @@ __global__ void __launch_bounds__(kThreads5, 1)
       tmem_wait_ld();
       // q columns [c_lo, c_hi) of this tile attend the key (relative to c0)
       const int row0 = g.row_offset + q0;
-      const int c_lo = max(0, key - row0) - c0;
+      const int c_lo = max(0, row_beg - row0) - c0;
       const int c_hi = min(min(kBwdQ, n_real - q0), row_end - row0) - c0;
       float p[32];
       const float4* l4 = reinterpret_cast<const float4*>(s.lse2[st] + c0);
@@ -503,9 +516,18 @@ __global__ void __launch_bounds__(kThreads5, 1)
           uint32_t kk[32];
           tmem_ld32(tbase + lane_off + kColDk + c, kk);
           tmem_wait_ld();
-          if (j < g.S_kv) {
+          const int pr = kSink ? unit_part_row(g, s.u_slot, s.u_flags, s.u_rbase, r) : -1;
+          if (j < g.S_kv && pr != -2) {
             const size_t off = kv_row(g, b, hk, j) * kD5 + slice * kSlice + c;
-            if (grads_bf16) {
+            if (kSink && pr >= 0) {  // a row that several units of the tile touch: the unit's partial slot
+              uint4* pv = reinterpret_cast<uint4*>(unit_part(g, s.u_slot, hk, 1, pr) + slice * kSlice + c);
+              uint4* pk4 = reinterpret_cast<uint4*>(unit_part(g, s.u_slot, hk, 0, pr) + slice * kSlice + c);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                pv[e] = make_uint4(vv[4 * e], vv[4 * e + 1], vv[4 * e + 2], vv[4 * e + 3]);
+                pk4[e] = make_uint4(kk[4 * e], kk[4 * e + 1], kk[4 * e + 2], kk[4 * e + 3]);
+              }
+            } else if (grads_bf16) {
               uint4* pv = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(dv) + off);
               uint4* pk4 = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(dk) + off);
 #pragma unroll
@@ -596,12 +618,16 @@ cudaError_t launch_bwd512_main(const CUtensorMap& mq, const CUtensorMap& mdo, co
                                cudaStream_t st) {
   if (g.D != kD5) return cudaErrorInvalidValue;
   const size_t smem = sizeof(Bwd512Smem) + 1024;  // + 1 KB to align the swizzled tiles
-  auto kern = g.drop_t ? (dq_acc ? bwd512_kernel<true, true> : bwd512_kernel<false, true>)
-                       : (dq_acc ? bwd512_kernel<true, false> : bwd512_kernel<false, false>);
+  auto kern = g.sink_tab ? (g.drop_t ? (dq_acc ? bwd512_kernel<true, true, true> : bwd512_kernel<false, true, true>)
+                                     : (dq_acc ? bwd512_kernel<true, false, true> : bwd512_kernel<false, false, true>))
+                         : (g.drop_t ? (dq_acc ? bwd512_kernel<true, true, false> : bwd512_kernel<false, true, false>)
+                                     : (dq_acc ? bwd512_kernel<true, false, false>
+                                               : bwd512_kernel<false, false, false>));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int reach = kv_tiles_reachable(g);
-  const long long grid = static_cast<long long>(g.B) * (reach > 0 ? reach : 1) * g.Hkv * kNSlice;
+  long long grid = static_cast<long long>(g.B) * (reach > 0 ? reach : 1) * g.Hkv * kNSlice;
+  if (g.sink_tab) grid = (g.sk_units > 0 ? g.sk_units : 1LL) * g.Hkv * kNSlice;
   if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (const cudaError_t le = launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads5), smem, st,
       mq, mdo, mk, mv, seg, g, lse, delta, dq_acc, dk, dv, bf16, status); le != cudaSuccess) return le;

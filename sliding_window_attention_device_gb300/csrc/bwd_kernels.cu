@@ -160,6 +160,7 @@ struct BwdSmem {
   uint32_t tmem_base;
   int abort_flag;
   int b, kt, q64_lo, nq64, n_real, skip, mode, n_att;
+  int u_flags, u_slot, u_rbase;  // kSink: the unit's flags, partial slot and first partial row
 };
 
 constexpr int kBwdThreads = 512;
@@ -169,7 +170,7 @@ constexpr int kBwdModeIdle = 0;  // past the attended tiles (their dK / dV zeroe
 constexpr int kBwdModeWork = 1;  // an attended K/V tile
 
 // kDq: with the dq products (else dK / dV only, for the fixed-order dq pass).
-template <int D, bool kDq, bool kDrop>
+template <int D, bool kDq, bool kDrop, bool kSink>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_dout,
                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -193,13 +194,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int item = blockIdx.x / g.Hkv;
   if (tid == 0) {
     // the attended K/V tiles lead the work list; the grid must cover them
+    // (kSink: units, which cover the attended tiles)
     const int n_att = seg[g.off[BD_SEG_OFF_COUNTS] + 3];
+    const int n_work = kSink ? sink_n_units(g, seg) : n_att;
     int mode = kBwdModeIdle;
     s.n_att = -1;
-    if (n_att < 0 || n_att > g.B * g.nkt || n_att > static_cast<int>(gridDim.x) / g.Hkv) {
+    if (n_att < 0 || n_att > g.B * g.nkt || n_work < n_att || n_work > static_cast<int>(gridDim.x) / g.Hkv) {
       atomicOr(status, BD_STATUS_BOUNDS);
     } else {
-      mode = item < n_att ? kBwdModeWork : kBwdModeIdle;
+      mode = item < n_work ? kBwdModeWork : kBwdModeIdle;
       s.n_att = n_att;
     }
     s.mode = mode;
@@ -220,16 +223,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 
   if (tid == 0) {
-    const int wi = seg[g.off[BD_SEG_OFF_BWD_WORK] + item];
+    const int32_t* u = kSink ? seg + g.sk_off + kSinkHdrWords + static_cast<size_t>(item) * kSinkUnitWords : nullptr;
+    const int wi = kSink ? u[0] : seg[g.off[BD_SEG_OFF_BWD_WORK] + item];
     int ok = wi >= 0 && wi < g.B * g.nkt;
     const int b = ok ? wi / g.nkt : 0, kt = ok ? wi % g.nkt : 0;
     const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
     ok = ok && hdr[kHdrMagic] == kSegMagic && hdr[kHdrRowOffset] == g.row_offset && hdr[kHdrL] == g.L &&
          hdr[kHdrKvOffset] == g.kv_offset && hdr[kHdrSkv] == g.S_kv && hdr[kHdrWindow] == g.window &&
-         hdr[kHdrSfull] == g.S_full;
+         hdr[kHdrSfull] == g.S_full && hdr[kHdrSink] == g.n_sink;
     const int n_real = hdr[BD_SEG_N_REAL];
     const int32_t* qr = seg + g.off[BD_SEG_OFF_KT_QRANGE] + (b * g.nkt + kt) * 2;
-    const int qlo = qr[0], qhi = qr[1];
+    const int qlo = kSink ? u[1] : qr[0], qhi = kSink ? u[2] : qr[1];
+    if constexpr (kSink) {
+      s.u_flags = u[3];
+      s.u_slot = u[4];
+      s.u_rbase = u[5];
+      ok = ok && u[4] < g.sk_slots && u[5] >= 0 && u[5] < kTile;
+    }
     // an attended tile has a non-empty q range
     ok = ok && n_real >= 0 && n_real <= g.L && qlo >= 0 && qhi <= n_real && qlo < qhi;
     const int nq64 = qhi > qlo ? (qhi - 1) / kBwdQ - qlo / kBwdQ + 1 : 0;
@@ -483,7 +493,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // rows attending s are [s, min(doc_end(s), s + W)) intersected with the
     // real rows. doc_end(s) is fixed for the CTA: find it once from cu_q.
     const int key = g.kv_offset + j;  // global position of this thread's key
-    int doc_end = -0x40000000;        // keys no local row attends
+    int doc_beg = 0, doc_end = -0x40000000;  // keys no local row attends
     {
       const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
       const int32_t* cu_q = seg + g.off[BD_SEG_OFF_CU_Q] + b * (g.L + 1);
@@ -499,12 +509,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           k = a;
         }
         doc_end = g.row_offset + cu_q[k + 1];
+        if constexpr (kSink) doc_beg = k == 0 ? hdr[BD_SEG_S_FIRST] : g.row_offset + cu_q[k];
       }
     }
     const int win_end = g.window > 0 ? key + g.window : 0x3fffffff;
-    const int row_end = min(doc_end, win_end);  // rows [key, row_end) attend this key
+    int row_beg = key, row_end = min(doc_end, win_end);  // rows [row_beg, row_end) attend this key
+    if constexpr (kSink)  // in this unit
+      unit_rows(g, key, doc_beg, doc_end, (s.u_flags & kUnitSink) != 0, &row_beg, &row_end);
     // dropout: scale * keep scale multiplies a kept dP (a dropped one is zero)
     const float sc_dp = kDrop ? g.scale * g.drop_scale : g.scale;
+    // 32 columns from `col` of this key's dk (which = 0) or dv (1) row; kSink:
+    // rows that several units of the tile touch go to the unit's partial slot
+    auto put = [&](int which, void* base, int col, const float* vals32) {
+      if constexpr (kSink) {
+        const int pr = unit_part_row(g, s.u_slot, s.u_flags, s.u_rbase, r);
+        if (pr == -2) return;
+        if (pr >= 0) {
+          float4* p4 = reinterpret_cast<float4*>(unit_part(g, s.u_slot, hk, which, pr) + col);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            p4[e] = make_float4(vals32[4 * e + 0], vals32[4 * e + 1], vals32[4 * e + 2], vals32[4 * e + 3]);
+          return;
+        }
+      }
+      store_row(base, kv_row(g, b, hk, j) * D + col, vals32);
+    };
     bool ok = true;
     for (int it = 0; it < n_it; ++it) {
       const int st = it & 1;  // slot of this tile's row values
@@ -523,7 +552,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tmem_wait_ld();
       // q columns [c_lo, c_hi) of this tile attend the key (relative to c0)
       const int row0 = g.row_offset + q0;
-      const int c_lo = max(0, key - row0) - c0;
+      const int c_lo = max(0, row_beg - row0) - c0;
       const int c_hi = min(min(kBwdQ, n_real - q0), row_end - row0) - c0;
       float p[32];
       const float4* l4 = reinterpret_cast<const float4*>(s.lse2[st] + c0);
@@ -595,14 +624,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const float dvs = kDrop ? g.drop_scale : 1.0f;  // dropout: the keep scale of P^T
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(vv[e]) * dvs;
-            store_row(dv, kv_row(g, b, hk, j) * D + pass * kDp + c, f);
+            put(1, dv, pass * kDp + c, f);
           }
           tmem_ld32(tbase + lane_off + Cfg::kColDk + c, vv);
           tmem_wait_ld();
           if (j < g.S_kv) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(vv[e]);  // dS was pre-scaled
-            store_row(dk, kv_row(g, b, hk, j) * D + pass * kDp + c, f);
+            put(0, dk, pass * kDp + c, f);
           }
         }
         tc_fence_before();
@@ -711,13 +740,15 @@ cudaError_t launch_main_d(const CUtensorMap& mq, const CUtensorMap& mdo, const C
                           const float* delta, float* dq_acc, void* dk, void* dv, int bf16, int32_t* status,
                           cudaStream_t st) {
   const size_t smem = sizeof(BwdSmem<D, BwdCfg<D>::kNsq>) + 1024;  // + 1 KB to align the swizzled tiles
-  auto kern = g.drop_t ? bwd_kernel<D, kDq, true> : bwd_kernel<D, kDq, false>;
+  auto kern = g.sink_tab ? (g.drop_t ? bwd_kernel<D, kDq, true, true> : bwd_kernel<D, kDq, false, true>)
+                         : (g.drop_t ? bwd_kernel<D, kDq, true, false> : bwd_kernel<D, kDq, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   // only tiles some local row can reach by position get a working CTA; with
   // none reachable, B CTAs per kv head still zero dK / dV
   const int reach = kv_tiles_reachable(g);
-  const long long grid = static_cast<long long>(g.B) * (reach > 0 ? reach : 1) * g.Hkv;
+  long long grid = static_cast<long long>(g.B) * (reach > 0 ? reach : 1) * g.Hkv;
+  if (g.sink_tab) grid = (g.sk_units > 0 ? g.sk_units : 1LL) * g.Hkv;
   if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (const cudaError_t le = launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), smem, st, mq,
       mdo, mk, mv, mdq, seg, g, lse, delta, dq_acc, dk, dv, bf16, status); le != cudaSuccess) return le;

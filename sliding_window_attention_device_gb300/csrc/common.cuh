@@ -23,6 +23,14 @@ struct Geom {
   uint32_t seed_lo, seed_hi;      // dropout: Philox key
   int nqt, nkt, nkw;              // 128-row q tiles, 128-row K/V tiles, bitmap words per q tile
   int off[BD_SEG_NOFF];           // word offsets of the table regions
+  int n_sink;                     // first keys of a document that stay visible past the window (0: none)
+  // sink tables only (sink_tab = 1): the regions behind the ordinary table
+  int sink_tab;
+  int sk_off;                     // word offset of the sink header (kSinkHdrWords), then the units, then the sums
+  int sk_units, sk_sums, sk_slots;  // capacities of the unit list, the sum list and the partial slots
+  int sk_rows;                    // key rows of a partial slot
+  int sk_split;                   // 128-row q tiles of a sink unit
+  float* sk_part;                 // partial slots of a backward, in the caller's workspace
 };
 
 __host__ __device__ inline int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -46,6 +54,22 @@ __host__ __device__ inline void seg_layout(int B, int L, int S_kv, int* off, int
   off[BD_SEG_OFF_COUNTS] = o;     o = align4(o + 8);
   off[BD_SEG_OFF_TOTAL] = o;
 }
+
+// ---- sink tables -----------------------------------------------------------
+// With a window W and n sink tokens, the visible pairs of a document split into
+// the window pairs (p - s < W) and the sink-only pairs (p - s >= W, s among the
+// document's first n keys). A K/V tile's window rows are a short range; its
+// sink-only rows run to the document's end. The backward therefore works on
+// units: one window unit per K/V tile that has window rows, and the sink-only
+// rows cut into units of sk_split q tiles. A K/V tile with one unit writes its
+// dk / dv directly; the units of a tile with several write the key rows that
+// more than one unit touches, [rbase, rbase + sk_rows), as fp32 partials into
+// slots of the workspace, which a last kernel adds in slot order.
+constexpr int kSinkHdrWords = 8;   // n_units, n_sums, n_slots
+constexpr int kSinkUnitWords = 8;  // item (b * nkt + kt), q_begin, q_end (local rows), flags, slot (-1: none), rbase
+constexpr int kSinkSumWords = 4;   // item, first slot, slots, rbase
+constexpr int kUnitSink = 1;       // the unit holds the sink-only pairs (else the window pairs)
+constexpr int kUnitPrimary = 2;    // also writes the tile's rows outside [rbase, rbase + sk_rows)
 
 // Row index of (batch row b, kv head hk, K/V buffer row j) in k, v, dk, dv.
 __host__ __device__ inline size_t kv_row(const Geom& g, int b, int hk, int j) {
@@ -75,13 +99,128 @@ __host__ __device__ inline long long plan_layout(int B, int W, int L, int* off) 
 // Header words that record the geometry the table was built for.
 constexpr int kHdrRowOffset = 16, kHdrL = 17, kHdrKvOffset = 18, kHdrSkv = 19, kHdrWindow = 20,
               kHdrSfull = 21, kHdrMagic = 22,
-              kHdrKvChunk = 23;  // 1: table built for one K/V chunk (no K/V range requirement)
+              kHdrKvChunk = 23,  // 1: table built for one K/V chunk (no K/V range requirement)
+              kHdrSink = 24,     // n_sink the table was built for (0 in ordinary tables)
+              kHdrSinkTab = 25;  // 1: the sink regions follow the table
 constexpr int kSegMagic = 0x62646174;  // "bdat"
 
 // The allowed key interval [lo, hi] (global positions) of a real local row i:
 // hi = p, lo = max(doc_start, p - W + 1).
 __device__ __forceinline__ int row_lo_window(int doc_start, int p, int window) {
   return (window > 0 && p - window + 1 > doc_start) ? p - window + 1 : doc_start;
+}
+
+// Capacities of a sink table and its partial slots. A K/V tile has sink-only
+// rows only if it holds sinks of a document with rows at distance >= W; for
+// W >= kTile these are the straddling document and documents longer than W, at
+// most 1 + L / W of them, each with its sinks (n <= 128) in at most two tiles,
+// and only the last document of a tile has rows behind the tile. For W < kTile
+// any tile may count, and a document's rows may lie within the tile itself.
+__host__ __device__ inline void sink_sizes(Geom* g) {
+  const bool on = g->window > 0 && g->n_sink > 0;
+  g->sk_rows = g->window >= kTile ? (g->n_sink > 0 ? g->n_sink : 1) : kTile;
+  const int w_tiles = g->window / kTile + 1;
+  g->sk_split = w_tiles > 4 ? w_tiles : 4;  // a sink unit no longer than a window unit, nor shorter than 4 tiles
+  long long t = 0, u = 0;
+  if (on) {
+    t = g->window >= kTile ? 2LL * (1 + g->L / g->window) : g->nkt;
+    if (t > g->nkt) t = g->nkt;
+    u = t + (2LL * g->nqt + 8 * t) / g->sk_split + 2;
+  }
+  // window units: the K/V tiles reachable by position through the window
+  const long long hi = static_cast<long long>(g->row_offset) + g->L - 1 - g->kv_offset;
+  const long long lo = g->window > 0 ? static_cast<long long>(g->row_offset) - g->window + 1 - g->kv_offset : 0;
+  const long long a = lo > 0 ? lo : 0;
+  const long long e = hi < g->S_kv - 1 ? hi : static_cast<long long>(g->S_kv) - 1;
+  const long long reach = e < a ? 0 : e / kTile - a / kTile + 1;
+  g->sk_sums = static_cast<int>(g->B * t);
+  g->sk_slots = static_cast<int>(g->B * (u + t));
+  g->sk_units = static_cast<int>(g->B * (reach + u));
+}
+
+// Words of the sink regions (each region a multiple of 4 words).
+__host__ __device__ inline long long sink_words(const Geom& g) {
+  return kSinkHdrWords + static_cast<long long>(g.sk_units) * kSinkUnitWords +
+         static_cast<long long>(g.sk_sums) * kSinkSumWords;
+}
+
+// K/V tiles of q tile qt that only its first document's sinks reach: its rows'
+// window ranges start at lo(first row) (tile kt_lo, n_main tiles, both clipped
+// to the buffer); the sinks before that lie in tiles [*x0, *x0 + *nx), all
+// below kt_lo. A document that starts inside the q tile starts behind lo(first
+// row), so its sinks are in the window range already.
+__device__ inline void sink_extra_tiles(const Geom& g, const int32_t* seg, int b, int qt, int n_real, int kt_lo,
+                                        int n_main, int* x0, int* nx) {
+  *x0 = 0;
+  *nx = 0;
+  const int first = qt * kTile;
+  if (g.window <= 0 || g.n_sink <= 0 || first >= n_real) return;
+  const int p = g.row_offset + first;
+  const int ds = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + first];
+  const int lo = p - g.window + 1;  // the first document's rows see no window key before it
+  if (ds < 0 || lo <= ds) return;
+  const int a = ds > g.kv_offset ? ds - g.kv_offset : 0;
+  int e = (ds + g.n_sink < lo ? ds + g.n_sink : lo) - 1 - g.kv_offset;
+  if (e > g.S_kv - 1) e = g.S_kv - 1;
+  if (e < a) return;
+  int t1 = e / kTile;
+  if (n_main > 0 && t1 > kt_lo - 1) t1 = kt_lo - 1;
+  const int t0 = a / kTile;
+  if (t1 < t0) return;
+  *x0 = t0;
+  *nx = t1 - t0 + 1;
+}
+
+// Visible keys of a row beside its window range [jlo, jhi]: its document's
+// sinks before it, buffer rows [*slo, *shi] (slo > shi: none). Sinks that touch
+// the window range join it.
+__device__ __forceinline__ void sink_interval(const Geom& g, int doc_start, int* jlo, int* slo, int* shi) {
+  *slo = 1;
+  *shi = 0;
+  if (g.window <= 0 || g.n_sink <= 0) return;
+  const int d = doc_start - g.kv_offset;
+  if (d >= *jlo) return;  // the window reaches the document's start
+  if (d + g.n_sink >= *jlo) {
+    *jlo = d;
+  } else {
+    *slo = d;
+    *shi = d + g.n_sink - 1 < g.S_kv - 1 ? d + g.n_sink - 1 : g.S_kv - 1;  // a K/V chunk may end among them
+  }
+}
+
+// Units of a sink table, or -1 when the table is not one for this geometry.
+__device__ __forceinline__ int sink_n_units(const Geom& g, const int32_t* seg) {
+  const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR];
+  if (hdr[kHdrMagic] != kSegMagic || hdr[kHdrSink] != g.n_sink || hdr[kHdrSinkTab] != 1 || hdr[kHdrL] != g.L ||
+      hdr[kHdrSkv] != g.S_kv || hdr[kHdrWindow] != g.window || hdr[kHdrRowOffset] != g.row_offset ||
+      hdr[kHdrKvOffset] != g.kv_offset)
+    return -1;  // the capacities, and so the regions' places, follow from these
+  const int n = seg[g.sk_off];
+  return n <= g.sk_units ? n : -1;
+}
+
+// Where key row r of a unit's tile goes: >= 0 a row of the unit's partial slot,
+// -1 straight to dk / dv, -2 nowhere (another unit of the tile writes it).
+__device__ __forceinline__ int unit_part_row(const Geom& g, int slot, int flags, int rbase, int r) {
+  if (slot < 0) return -1;
+  if (r >= rbase && r < rbase + g.sk_rows) return r - rbase;
+  return (flags & kUnitPrimary) ? -1 : -2;
+}
+// A slot row of dk (which = 0) or dv (1) of kv head hk.
+__device__ __forceinline__ float* unit_part(const Geom& g, int slot, int hk, int which, int row) {
+  return g.sk_part + (((static_cast<size_t>(slot) * g.Hkv + hk) * 2 + which) * g.sk_rows + row) * g.D;
+}
+
+// The rows [beg, end) (global positions) that attend key `key` (doc [ds, de))
+// in a unit: window pairs s <= p < s + W, or sink-only pairs p >= s + W.
+__device__ __forceinline__ void unit_rows(const Geom& g, int key, int ds, int de, bool sink_unit, int* beg, int* end) {
+  if (sink_unit) {
+    *beg = key + g.window;
+    *end = key - ds < g.n_sink ? de : -0x40000000;
+  } else {
+    *beg = key;
+    *end = g.window > 0 && key + g.window < de ? key + g.window : de;
+  }
 }
 
 // Number of 128-row K/V tiles some local row can attend by position alone:

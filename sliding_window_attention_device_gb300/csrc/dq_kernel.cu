@@ -48,12 +48,13 @@ struct DqSmem {
   uint32_t tmem_base;
   int abort_flag;
   int b, qt, kt_lo, nk, n_real, skip;
+  int x0, nx;  // K/V tiles of the first document's sinks, walked before the window's
 };
 
 constexpr uint32_t kColS = 0, kColDp = 128, kColDq = 256;
 constexpr int kDqThreads = 256;
 
-template <int D, int NS, bool kDrop>
+template <int D, int NS, bool kDrop, bool kSink>
 __global__ void __launch_bounds__(kDqThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_dout,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -76,16 +77,24 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
     ok = ok && hdr[kHdrMagic] == kSegMagic && hdr[kHdrRowOffset] == g.row_offset && hdr[kHdrL] == g.L &&
          hdr[kHdrKvOffset] == g.kv_offset && hdr[kHdrSkv] == g.S_kv && hdr[kHdrWindow] == g.window &&
-         hdr[kHdrSfull] == g.S_full;
+         hdr[kHdrSfull] == g.S_full && hdr[kHdrSink] == g.n_sink;
     const int n_real = hdr[BD_SEG_N_REAL];
     const int32_t* kr = seg + g.off[BD_SEG_OFF_QT_KRANGE] + (b * g.nqt + qt) * 2;
     const int kt_lo = kr[0], kt_hi = kr[1];
-    const int nk = kt_hi >= kt_lo ? kt_hi - kt_lo + 1 : 0;
+    int nk = kt_hi >= kt_lo ? kt_hi - kt_lo + 1 : 0;
     ok = ok && n_real >= 0 && n_real <= g.L && (nk == 0 || (kt_lo >= 0 && kt_hi < g.nkt));
     if (!ok) atomicOr(status, BD_STATUS_BOUNDS);
     s.b = b;
     s.qt = qt;
-    s.kt_lo = kt_lo;
+    if constexpr (kSink) {
+      // nk counts the sink tiles too: tile j is x0 + j below nx, kt_lo + j - nx above
+      s.x0 = s.nx = 0;
+      if (ok) sink_extra_tiles(g, seg, b, qt, n_real, kt_lo, nk, &s.x0, &s.nx);
+      nk += s.nx;
+      s.kt_lo = kt_lo - s.nx;
+    } else {
+      s.kt_lo = kt_lo;
+    }
     s.nk = nk;
     s.n_real = n_real;
     s.skip = (!ok || *vstatus != 0) ? 1 : 0;
@@ -108,6 +117,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   __syncthreads();
   if (s.skip) return;
   const int b = s.b, qt = s.qt, kt_lo = s.kt_lo, nk = s.nk, n_real = s.n_real;
+  const int x0 = kSink ? s.x0 : 0, nx = kSink ? s.nx : 0;
+  auto tile_of = [&](int j) { return kSink && j < nx ? x0 + j : kt_lo + j; };
   const size_t row0 = (static_cast<size_t>(b) * g.Hq + h) * g.L;  // dq / lse / delta row of local row 0
 
   if (nk == 0) {  // no row of this q tile sees a key: dq = 0
@@ -144,7 +155,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     int issued = 0;
     for (int j = 0; j < nk; ++j) {
       const int st = j % NS, n = j / NS;
-      const int row = (kt_lo + j) * kTile, pl = b * g.Hkv + hk;
+      const int row = tile_of(j) * kTile, pl = b * g.Hkv + hk;
       if (j >= NS && !(pipe_wait(&s.k_empty[st], (n - 1) & 1, &s.abort_flag, vstatus) &&
                        pipe_wait(&s.v_empty[st], (n - 1) & 1, &s.abort_flag, vstatus)))
         break;
@@ -235,12 +246,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const int i = qt * kTile + r;
     const bool real = i < n_real;
     int jlo = 1, jhi = 0;  // allowed K/V buffer rows [jlo, jhi] of this row
+    int slo = 1, shi = 0;  // kSink: and its document's sinks [slo, shi] before them
     float nl2 = 0.f, ndl = 0.f;
     if (real) {
       const int p = g.row_offset + i;
       const int doc_start = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + i];
       jlo = row_lo_window(doc_start, p, g.window) - g.kv_offset;
       jhi = min(p - g.kv_offset, g.S_kv - 1);  // a K/V chunk may end before the row
+      if constexpr (kSink) sink_interval(g, doc_start, &jlo, &slo, &shi);
       nl2 = lse[row0 + i] * -1.4426950408889634f;
       ndl = delta[row0 + i] * -g.scale;  // dS is formed pre-scaled: scale * P (dP - delta)
     }
@@ -250,17 +263,32 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     bool ok = true;
     for (int j = 0; j < nk; ++j) {
       uint32_t km[4];  // dropout: keep bits of this row over the tile's 128 keys
-      if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + (kt_lo + j) * kTile, km);
+      if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + tile_of(j) * kTile, km);
       if (!warp_wait(&s.sdp_full, j & 1, &s.abort_flag, vstatus)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const int c0 = (kt_lo + j) * kTile;
+      const int c0 = tile_of(j) * kTile;
       // a row sees all of this tile, none of it, or part of it
-      const bool dead = !real || jhi < c0 || jlo > c0 + kTile - 1;
-      const bool full = jlo <= c0 && c0 + kTile - 1 <= jhi;
-      const int a_lo = jlo - c0, e_hi = jhi - c0;
+      // kSink: a row sees the tile through its window or its sinks; both at
+      // once only where the sinks end in the window's first tile
+      int wlo = jlo, whi = jhi, b_lo = 1, b_hi = 0;
+      if constexpr (kSink) {
+        if (shi >= c0 && slo <= c0 + kTile - 1 && slo <= shi) {
+          if (jhi < c0 || jlo > c0 + kTile - 1) {
+            wlo = slo;
+            whi = shi;
+          } else {
+            b_lo = slo - c0;
+            b_hi = shi - c0;
+          }
+        }
+      }
+      const bool dead = !real || whi < c0 || wlo > c0 + kTile - 1;
+      const bool full = wlo <= c0 && c0 + kTile - 1 <= whi;
+      const int a_lo = wlo - c0, e_hi = whi - c0;
+      auto sees = [&](int c) { return (c >= a_lo && c <= e_hi) || (kSink && c >= b_lo && c <= b_hi); };
       uint32_t pk[2][32];  // dS of keys [64 hf, 64 hf + 64), bf16 pairs
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -285,8 +313,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             p0 = 0.f;
             p1 = 0.f;
           } else if (!full) {
-            p0 = (c >= a_lo && c <= e_hi) ? p0 : 0.f;
-            p1 = (c + 1 >= a_lo && c + 1 <= e_hi) ? p1 : 0.f;
+            p0 = sees(c) ? p0 : 0.f;
+            p1 = sees(c + 1) ? p1 : 0.f;
           }
           float dp0 = __uint_as_float(dr[2 * e]), dp1 = __uint_as_float(dr[2 * e + 1]);
           if constexpr (kDrop) {
@@ -366,7 +394,8 @@ cudaError_t launch_dq(const CUtensorMap& mq, const CUtensorMap& mdo, const CUten
   e = cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e != cudaSuccess) return e;
   if (smem > static_cast<size_t>(max_optin)) return cudaErrorInvalidValue;
-  auto kern = g.drop_t ? bwd_dq_kernel<D, NS, true> : bwd_dq_kernel<D, NS, false>;
+  auto kern = g.n_sink ? (g.drop_t ? bwd_dq_kernel<D, NS, true, true> : bwd_dq_kernel<D, NS, false, true>)
+                       : (g.drop_t ? bwd_dq_kernel<D, NS, true, false> : bwd_dq_kernel<D, NS, false, false>);
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(g.B) * g.nqt * g.Hq;  // (q tile, query head)

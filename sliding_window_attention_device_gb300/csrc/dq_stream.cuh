@@ -18,10 +18,13 @@ namespace bd {
 // row's S and dP columns in tensor memory (128 each); nl2 = -lse log2(e),
 // ndl = -scale delta. With attention dropout (kDrop), key c's dP counts only
 // when bit c of km is set and is scaled by drop_scale: dS = P (Z dP - delta).
-template <bool kDrop = false>
+// kSink: the keys [b_lo, b_hi] are allowed too.
+template <bool kDrop = false, bool kSink = false>
 __device__ __forceinline__ void dq_form_ds(uint32_t t_s, uint32_t t_dp, float scale, float nl2, float ndl,
                                            bool dead, bool full, int a_lo, int e_hi, uint32_t (&pk)[2][32],
-                                           const uint32_t (&km)[4] = {0u, 0u, 0u, 0u}, float drop_scale = 1.0f) {
+                                           const uint32_t (&km)[4] = {0u, 0u, 0u, 0u}, float drop_scale = 1.0f,
+                                           int b_lo = 1, int b_hi = 0) {
+  auto sees = [&](int c) { return (c >= a_lo && c <= e_hi) || (kSink && c >= b_lo && c <= b_hi); };
   const float2 sl2 = make_float2(scale * 1.4426950408889634f, scale * 1.4426950408889634f);
   const float scd = kDrop ? scale * drop_scale : scale;
   const float2 sc = make_float2(scd, scd), nl2v = make_float2(nl2, nl2), ndlv = make_float2(ndl, ndl);
@@ -44,8 +47,8 @@ __device__ __forceinline__ void dq_form_ds(uint32_t t_s, uint32_t t_dp, float sc
         p0 = 0.f;
         p1 = 0.f;
       } else if (!full) {
-        p0 = (c >= a_lo && c <= e_hi) ? p0 : 0.f;
-        p1 = (c + 1 >= a_lo && c + 1 <= e_hi) ? p1 : 0.f;
+        p0 = sees(c) ? p0 : 0.f;
+        p1 = sees(c + 1) ? p1 : 0.f;
       }
       float dp0 = __uint_as_float(dr[2 * e]), dp1 = __uint_as_float(dr[2 * e + 1]);
       if constexpr (kDrop) {

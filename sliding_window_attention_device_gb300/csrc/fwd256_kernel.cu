@@ -50,13 +50,14 @@ struct Fwd256Smem {
   uint32_t tmem_base;
   int abort_flag;
   int b, qt, kt_lo, nk, n_real, skip;
+  int x0, nx;  // K/V tiles of the first document's sinks, walked before the window's
 };
 static_assert(sizeof(Fwd256Smem) + 1024 <= 232448, "shared memory per CTA");
 static_assert(2 * 2 * kChunkB256 >= kTile * kD256 * 2, "out staging fits ring slots 0-1");
 
 // kMerge: merge this K/V chunk's result into the running (out, lse) instead
 // of writing it (log-sum-exp weights, as the merge kernel).
-template <bool kMerge, bool kDrop>
+template <bool kMerge, bool kDrop, bool kSink>
 __global__ void __launch_bounds__(kThreadsF256, 1)
     fwd256_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const int32_t* __restrict__ seg, const Geom g,
@@ -76,16 +77,24 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
     const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
     ok = ok && hdr[kHdrMagic] == kSegMagic && hdr[kHdrRowOffset] == g.row_offset && hdr[kHdrL] == g.L &&
          hdr[kHdrKvOffset] == g.kv_offset && hdr[kHdrSkv] == g.S_kv && hdr[kHdrWindow] == g.window &&
-         hdr[kHdrSfull] == g.S_full;
+         hdr[kHdrSfull] == g.S_full && hdr[kHdrSink] == g.n_sink;
     const int n_real = hdr[BD_SEG_N_REAL];
     const int32_t* kr = seg + g.off[BD_SEG_OFF_QT_KRANGE] + (b * g.nqt + qt) * 2;
     const int kt_lo = kr[0], kt_hi = kr[1];
-    const int nk = kt_hi >= kt_lo ? kt_hi - kt_lo + 1 : 0;
+    int nk = kt_hi >= kt_lo ? kt_hi - kt_lo + 1 : 0;
     ok = ok && n_real >= 0 && n_real <= g.L && (nk == 0 || (kt_lo >= 0 && kt_hi < g.nkt));
     if (!ok) atomicOr(status, BD_STATUS_BOUNDS);
     s.b = b;
     s.qt = qt;
-    s.kt_lo = kt_lo;
+    if constexpr (kSink) {
+      // nk counts the sink tiles too: tile j is x0 + j below nx, kt_lo + j - nx above
+      s.x0 = s.nx = 0;
+      if (ok) sink_extra_tiles(g, seg, b, qt, n_real, kt_lo, nk, &s.x0, &s.nx);
+      nk += s.nx;
+      s.kt_lo = kt_lo - s.nx;
+    } else {
+      s.kt_lo = kt_lo;
+    }
     s.nk = nk;
     s.n_real = n_real;
     s.skip = (!ok || *vstatus != 0) ? 1 : 0;
@@ -113,7 +122,7 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
       for (int c = 0; c < kQChunks256; ++c) tma_load_3d(s.q[c], &tm_q, &s.q_full, c * 64, qt * kTile, b * g.Hq + h);
       const int pl = b * g.Hkv + hk;
       for (int x = 0; x < (nk < 2 ? 2 : 4); ++x) {
-        const int row = (kt_lo + (x >> 1)) * kTile, half = x & 1;
+        const int row = (kSink && (x >> 1) < s.nx ? s.x0 + (x >> 1) : s.kt_lo + (x >> 1)) * kTile, half = x & 1;
         mbar_arrive_expect_tx(&s.full[x], 2 * kChunkB256);
         for (int c = 0; c < 2; ++c)
           tma_load_3d(s.ring[x][c], &tm_k, &s.full[x], (2 * half + c) * 64, g.kv_tm ? pl : row, g.kv_tm ? row : pl);
@@ -123,6 +132,8 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
   __syncthreads();
   if (s.skip) return;
   const int b = s.b, qt = s.qt, kt_lo = s.kt_lo, nk = s.nk, n_real = s.n_real;
+  const int x0 = kSink ? s.x0 : 0, nx = kSink ? s.nx : 0;
+  auto tile_of = [&](int j) { return kSink && j < nx ? x0 + j : kt_lo + j; };
 
   if (nk == 0) {  // no row of this q tile sees a key: zeros and -inf
     if (tid >= 128) {
@@ -159,7 +170,7 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
       if (u >= kSlots256 && !pipe_wait(&s.empty[slot], (u / kSlots256 - 1) & 1, &s.abort_flag, vstatus))
         return false;
       mbar_arrive_expect_tx(&s.full[slot], 2 * kChunkB256);
-      const int row = (kt_lo + t) * kTile;
+      const int row = tile_of(t) * kTile;
       for (int c = 0; c < 2; ++c)
         tma_load_3d(s.ring[slot][c], map, &s.full[slot], (2 * half + c) * 64, g.kv_tm ? pl : row, g.kv_tm ? row : pl);
       ++u;
@@ -249,18 +260,20 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
     const int i = qt * kTile + r;
     const bool real = i < n_real;
     int jlo = 1, jhi = 0;  // allowed K/V buffer rows [jlo, jhi] of this row
+    int slo = 1, shi = 0;  // kSink: and its document's sinks [slo, shi] before them
     if (real) {
       const int p = g.row_offset + i;
       const int doc_start = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + i];
       jlo = row_lo_window(doc_start, p, g.window) - g.kv_offset;
       jhi = min(p - g.kv_offset, g.S_kv - 1);  // a K/V chunk may end before the row
+      if constexpr (kSink) sink_interval(g, doc_start, &jlo, &slo, &shi);
     }
     const float sl2 = g.scale * 1.4426950408889634f;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int t = 0; t < nk; ++t) {
       uint32_t km[4];  // dropout: keep bits of this row over the tile's 128 keys
-      if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + (kt_lo + t) * kTile, km);
+      if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + tile_of(t) * kTile, km);
       if (!warp_wait(&s.s_full[t & 1], (t >> 1) & 1, &s.abort_flag, vstatus)) {
         ok = false;
         break;
@@ -276,12 +289,26 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
       tmem_regs_ready<64>(&xr[0]);
       tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&xr[64]));
       tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&xr[96]));
-      const int c0 = (kt_lo + t) * kTile;
+      const int c0 = tile_of(t) * kTile;
       // a row either sees the whole tile, none of it, or part of it; only a
       // warp with a partly seen row needs the per-element mask
-      const bool dead = jhi < c0 || jlo > c0 + kTile - 1;
-      const bool unmasked = __all_sync(0xffffffffu, dead || (jlo <= c0 && c0 + kTile - 1 <= jhi));
-      const int a_lo = jlo - c0, e_hi = jhi - c0;
+      // (kSink: a row sees the tile through its window or its sinks; both at
+      // once only where the sinks end in the window's first tile)
+      int wlo = jlo, whi = jhi;
+      bool both = false;
+      if constexpr (kSink) {
+        if (shi >= c0 && slo <= c0 + kTile - 1 && slo <= shi) {
+          both = !(jhi < c0 || jlo > c0 + kTile - 1);
+          if (!both) {
+            wlo = slo;
+            whi = shi;
+          }
+        }
+        both = __any_sync(0xffffffffu, both);
+      }
+      const bool dead = whi < c0 || wlo > c0 + kTile - 1;
+      const bool unmasked = __all_sync(0xffffffffu, dead || (wlo <= c0 && c0 + kTile - 1 <= whi));
+      const int a_lo = wlo - c0, e_hi = whi - c0;
       float x[128];  // raw scores, -inf where masked
       float mx[8];   // eight independent 16-column maxima (short dependency chains)
 #pragma unroll
@@ -296,6 +323,14 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
         } else {
 #pragma unroll
           for (int c = 64 * hf; c < 64 * hf + 64; ++c) x[c] = (c >= a_lo && c <= e_hi) ? __uint_as_float(xr[c]) : -INFINITY;
+          if constexpr (kSink) {
+            if (both) {
+              const int b_lo = slo - c0, b_hi = shi - c0;
+#pragma unroll
+              for (int c = 64 * hf; c < 64 * hf + 64; ++c)
+                if (c >= b_lo && c <= b_hi) x[c] = __uint_as_float(xr[c]);
+            }
+          }
         }
 #pragma unroll
         for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
@@ -478,8 +513,10 @@ cudaError_t launch_fwd256(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   e = cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e != cudaSuccess) return e;
   if (smem > static_cast<size_t>(max_optin)) return cudaErrorInvalidValue;
-  auto kern = g.drop_t ? (merge ? fwd256_kernel<true, true> : fwd256_kernel<false, true>)
-                       : (merge ? fwd256_kernel<true, false> : fwd256_kernel<false, false>);
+  auto kern = g.n_sink ? (g.drop_t ? (merge ? fwd256_kernel<true, true, true> : fwd256_kernel<false, true, true>)
+                                   : (merge ? fwd256_kernel<true, false, true> : fwd256_kernel<false, false, true>))
+                       : (g.drop_t ? (merge ? fwd256_kernel<true, true, false> : fwd256_kernel<false, true, false>)
+                                   : (merge ? fwd256_kernel<true, false, false> : fwd256_kernel<false, false, false>));
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(g.B) * g.nqt * g.Hq;  // (q tile, query head)

@@ -50,11 +50,12 @@ struct Fwd512Smem {
   uint32_t tmem_base;
   int abort_flag;
   int b, qt, kt_lo, nk, n_real, skip;
+  int x0, nx;  // K/V tiles of the first document's sinks, walked before the window's
 };
 
 // kMerge: merge this K/V chunk's result into the running (out, lse) instead
 // of writing it (log-sum-exp weights, as the merge kernel).
-template <bool kMerge, bool kDrop>
+template <bool kMerge, bool kDrop, bool kSink>
 __global__ void __launch_bounds__(kThreads512, 1)
     fwd512_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const int32_t* __restrict__ seg, const Geom g,
@@ -75,16 +76,24 @@ __global__ void __launch_bounds__(kThreads512, 1)
     const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
     ok = ok && hdr[kHdrMagic] == kSegMagic && hdr[kHdrRowOffset] == g.row_offset && hdr[kHdrL] == g.L &&
          hdr[kHdrKvOffset] == g.kv_offset && hdr[kHdrSkv] == g.S_kv && hdr[kHdrWindow] == g.window &&
-         hdr[kHdrSfull] == g.S_full;
+         hdr[kHdrSfull] == g.S_full && hdr[kHdrSink] == g.n_sink;
     const int n_real = hdr[BD_SEG_N_REAL];
     const int32_t* kr = seg + g.off[BD_SEG_OFF_QT_KRANGE] + (b * g.nqt + qt) * 2;
     const int kt_lo = kr[0], kt_hi = kr[1];
-    const int nk = kt_hi >= kt_lo ? kt_hi - kt_lo + 1 : 0;
+    int nk = kt_hi >= kt_lo ? kt_hi - kt_lo + 1 : 0;
     ok = ok && n_real >= 0 && n_real <= g.L && (nk == 0 || (kt_lo >= 0 && kt_hi < g.nkt));
     if (!ok) atomicOr(status, BD_STATUS_BOUNDS);
     s.b = b;
     s.qt = qt;
-    s.kt_lo = kt_lo;
+    if constexpr (kSink) {
+      // nk counts the sink tiles too: tile j is x0 + j below nx, kt_lo + j - nx above
+      s.x0 = s.nx = 0;
+      if (ok) sink_extra_tiles(g, seg, b, qt, n_real, kt_lo, nk, &s.x0, &s.nx);
+      nk += s.nx;
+      s.kt_lo = kt_lo - s.nx;
+    } else {
+      s.kt_lo = kt_lo;
+    }
     s.nk = nk;
     s.n_real = n_real;
     s.skip = (!ok || *vstatus != 0) ? 1 : 0;
@@ -108,6 +117,8 @@ __global__ void __launch_bounds__(kThreads512, 1)
   __syncthreads();
   if (s.skip) return;
   const int b = s.b, qt = s.qt, kt_lo = s.kt_lo, nk = s.nk, n_real = s.n_real;
+  const int x0 = kSink ? s.x0 : 0, nx = kSink ? s.nx : 0;
+  auto tile_of = [&](int j) { return kSink && j < nx ? x0 + j : kt_lo + j; };
 
   if (nk == 0) {  // no row of this q tile sees a key: zeros and -inf
     if (tid >= 128) {
@@ -146,7 +157,7 @@ __global__ void __launch_bounds__(kThreads512, 1)
     bool stop = false;
     // K of step u (8 chunks through the ring)
     auto load_k = [&](int u) {
-      const int row = (kt_lo + u % nk) * kTile;
+      const int row = tile_of(u % nk) * kTile;
       for (int c = 0; c < kQChunks; ++c, ++kc) {
         const int slot = kc % kKSlots;
         if (kc >= kKSlots && !pipe_wait(&s.k_empty[slot], (kc / kKSlots - 1) & 1, &s.abort_flag, vstatus))
@@ -167,7 +178,7 @@ __global__ void __launch_bounds__(kThreads512, 1)
         stop = true;
         break;
       }
-      const int row = (kt_lo + t % nk) * kTile, p = t / nk;
+      const int row = tile_of(t % nk) * kTile, p = t / nk;
       mbar_arrive_expect_tx(&s.v_full, kVChunks * kChunkB);
       for (int c = 0; c < kVChunks; ++c)
         tma_load_3d(s.v[c], &tm_v, &s.v_full, (kVChunks * p + c) * 64, g.kv_tm ? pl : row, g.kv_tm ? row : pl);
@@ -243,11 +254,13 @@ __global__ void __launch_bounds__(kThreads512, 1)
     const int i = qt * kTile + r;
     const bool real = i < n_real;
     int jlo = 1, jhi = 0;  // allowed K/V buffer rows [jlo, jhi] of this row
+    int slo = 1, shi = 0;  // kSink: and its document's sinks [slo, shi] before them
     if (real) {
       const int p = g.row_offset + i;
       const int doc_start = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + i];
       jlo = row_lo_window(doc_start, p, g.window) - g.kv_offset;
       jhi = min(p - g.kv_offset, g.S_kv - 1);
+      if constexpr (kSink) sink_interval(g, doc_start, &jlo, &slo, &shi);
     }
     const size_t row = (static_cast<size_t>(b) * g.Hq + h) * g.L + i;
     const float sl2 = g.scale * 1.4426950408889634f;
@@ -262,7 +275,7 @@ __global__ void __launch_bounds__(kThreads512, 1)
     for (int p = 0; p < 2 && ok; ++p) {
       for (int j = 0; j < nk; ++j, ++t) {
         uint32_t km[4];  // dropout: keep bits of this row over the tile's 128 keys
-        if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + (kt_lo + j) * kTile, km);
+        if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + tile_of(j) * kTile, km);
         if (!warp_wait(&s.s_full[t & 1], (t >> 1) & 1, &s.abort_flag, vstatus)) {
           ok = false;
           break;
@@ -276,17 +289,32 @@ __global__ void __launch_bounds__(kThreads512, 1)
         tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&xr[96]));
         tmem_wait_ld();
         tmem_regs_ready<128>(xr);
-        const int c0 = (kt_lo + j) * kTile;
-        const bool dead = jhi < c0 || jlo > c0 + kTile - 1;
-        const bool full = jlo <= c0 && c0 + kTile - 1 <= jhi;
-        const int a_lo = jlo - c0, e_hi = jhi - c0;
+        const int c0 = tile_of(j) * kTile;
+        // kSink: a row sees the tile through its window or its sinks; both at
+        // once only where the sinks end in the window's first tile
+        int wlo = jlo, whi = jhi, b_lo = 1, b_hi = 0;
+        if constexpr (kSink) {
+          if (shi >= c0 && slo <= c0 + kTile - 1 && slo <= shi) {
+            if (jhi < c0 || jlo > c0 + kTile - 1) {
+              wlo = slo;
+              whi = shi;
+            } else {
+              b_lo = slo - c0;
+              b_hi = shi - c0;
+            }
+          }
+        }
+        const bool dead = whi < c0 || wlo > c0 + kTile - 1;
+        const bool full = wlo <= c0 && c0 + kTile - 1 <= whi;
+        const int a_lo = wlo - c0, e_hi = whi - c0;
+        auto sees = [&](int c) { return (c >= a_lo && c <= e_hi) || (kSink && c >= b_lo && c <= b_hi); };
         float nmm;  // exponent offset
         if (p == 0) {
           float tmax = -INFINITY;
           if (!dead) {
 #pragma unroll
             for (int c = 0; c < 128; ++c)
-              if (full || (c >= a_lo && c <= e_hi)) tmax = fmaxf(tmax, __uint_as_float(xr[c]));
+              if (full || sees(c)) tmax = fmaxf(tmax, __uint_as_float(xr[c]));
             tmax *= sl2;
           }
           const float m_new = fmaxf(m, tmax);
@@ -336,8 +364,8 @@ __global__ void __launch_bounds__(kThreads512, 1)
             p0 = 0.f;
             p1 = 0.f;
           } else if (!full) {
-            p0 = (2 * c >= a_lo && 2 * c <= e_hi) ? p0 : 0.f;
-            p1 = (2 * c + 1 >= a_lo && 2 * c + 1 <= e_hi) ? p1 : 0.f;
+            p0 = sees(2 * c) ? p0 : 0.f;
+            p1 = sees(2 * c + 1) ? p1 : 0.f;
           }
           rs2 = __fadd2_rn(rs2, make_float2(p0, p1));
           if constexpr (kDrop) {
@@ -442,8 +470,10 @@ cudaError_t launch_fwd512(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   e = cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e != cudaSuccess) return e;
   if (smem > static_cast<size_t>(max_optin)) return cudaErrorInvalidValue;
-  auto kern = g.drop_t ? (merge ? fwd512_kernel<true, true> : fwd512_kernel<false, true>)
-                       : (merge ? fwd512_kernel<true, false> : fwd512_kernel<false, false>);
+  auto kern = g.n_sink ? (g.drop_t ? (merge ? fwd512_kernel<true, true, true> : fwd512_kernel<false, true, true>)
+                                   : (merge ? fwd512_kernel<true, false, true> : fwd512_kernel<false, false, true>))
+                       : (g.drop_t ? (merge ? fwd512_kernel<true, true, false> : fwd512_kernel<false, true, false>)
+                                   : (merge ? fwd512_kernel<true, false, false> : fwd512_kernel<false, false, false>));
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(g.B) * g.nqt * g.Hq;  // (q tile, query head)

@@ -52,6 +52,7 @@ struct FwdSmem {
   int abort_flag;
   // work item, decoded by thread 0
   int b, qt, kt_lo, nk, n_real, skip;
+  int x0, nx;  // K/V tiles of the first document's sinks, walked before the window's
 };
 
 template <int D, int NQ>
@@ -63,7 +64,7 @@ struct FwdTmem {
   static_assert(kUsed <= 512, "tensor memory budget");
 };
 
-template <int D, int NQ, int NS, bool kMerge, bool kDrop>
+template <int D, int NQ, int NS, bool kMerge, bool kDrop, bool kSink>
 __global__ void __launch_bounds__(128 + NQ * 128, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const int32_t* __restrict__ seg, const Geom g,
@@ -89,16 +90,24 @@ __global__ void __launch_bounds__(128 + NQ * 128, 1)
     const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
     ok = ok && hdr[kHdrMagic] == kSegMagic && hdr[kHdrRowOffset] == g.row_offset && hdr[kHdrL] == g.L &&
          hdr[kHdrKvOffset] == g.kv_offset && hdr[kHdrSkv] == g.S_kv && hdr[kHdrWindow] == g.window &&
-         hdr[kHdrSfull] == g.S_full;
+         hdr[kHdrSfull] == g.S_full && hdr[kHdrSink] == g.n_sink;
     const int n_real = hdr[BD_SEG_N_REAL];
     const int32_t* kr = seg + g.off[BD_SEG_OFF_QT_KRANGE] + (b * g.nqt + qt) * 2;
     const int kt_lo = kr[0], kt_hi = kr[1];
-    const int nk = kt_hi >= kt_lo ? kt_hi - kt_lo + 1 : 0;
+    int nk = kt_hi >= kt_lo ? kt_hi - kt_lo + 1 : 0;
     ok = ok && n_real >= 0 && n_real <= g.L && (nk == 0 || (kt_lo >= 0 && kt_hi < g.nkt));
     if (!ok) atomicOr(status, BD_STATUS_BOUNDS);
     s.b = b;
     s.qt = qt;
-    s.kt_lo = kt_lo;
+    if constexpr (kSink) {
+      // nk counts the sink tiles too: tile j is x0 + j below nx, kt_lo + j - nx above
+      s.x0 = s.nx = 0;
+      if (ok) sink_extra_tiles(g, seg, b, qt, n_real, kt_lo, nk, &s.x0, &s.nx);
+      nk += s.nx;
+      s.kt_lo = kt_lo - s.nx;
+    } else {
+      s.kt_lo = kt_lo;
+    }
     s.nk = nk;
     s.n_real = n_real;
     s.skip = (!ok || *vstatus != 0) ? 1 : 0;
@@ -129,7 +138,7 @@ __global__ void __launch_bounds__(128 + NQ * 128, 1)
         for (int c = 0; c < kChunks; ++c)
           tma_load_3d(s.q[qi][c], &tm_q, &s.q_full, c * 64, qt * kTile, b * g.Hq + h0e + qi);
       for (int j = 0; j < NS && j < nk; ++j) {
-        const int row = (kt_lo + j) * kTile, pl = b * g.Hkv + hke;
+        const int row = (kSink && j < s.nx ? s.x0 + j : s.kt_lo + j) * kTile, pl = b * g.Hkv + hke;
         mbar_arrive_expect_tx(&s.k_full[j], kChunks * Smem::kChunkBytes);
         for (int c = 0; c < kChunks; ++c)
           tma_load_3d(s.k[j][c], &tm_k, &s.k_full[j], c * 64, g.kv_tm ? pl : row, g.kv_tm ? row : pl);
@@ -143,6 +152,8 @@ __global__ void __launch_bounds__(128 + NQ * 128, 1)
   if (s.skip) return;
   const int b = s.b, qt = s.qt, kt_lo = s.kt_lo, nk = s.nk, n_real = s.n_real;
   const int h0 = pair * NQ, hk = h0 / g.G;
+  const int x0 = kSink ? s.x0 : 0, nx = kSink ? s.nx : 0;
+  auto tile_of = [&](int j) { return kSink && j < nx ? x0 + j : kt_lo + j; };
 
   if (nk == 0) {
     // No row of this q tile sees a key: zeros and -inf (merging: a running
@@ -181,13 +192,13 @@ __global__ void __launch_bounds__(128 + NQ * 128, 1)
         break;
       mbar_arrive_expect_tx(&s.k_full[st], kChunks * Smem::kChunkBytes);
       for (int c = 0; c < kChunks; ++c)
-        tma_load_3d(s.k[st][c], &tm_k, &s.k_full[st], c * 64, g.kv_tm ? b * g.Hkv + hk : (kt_lo + j) * kTile, g.kv_tm ? (kt_lo + j) * kTile : b * g.Hkv + hk);
+        tma_load_3d(s.k[st][c], &tm_k, &s.k_full[st], c * 64, g.kv_tm ? b * g.Hkv + hk : tile_of(j) * kTile, g.kv_tm ? tile_of(j) * kTile : b * g.Hkv + hk);
       ++k_issued;
       if (j >= NS && !pipe_wait(&s.v_empty[st], (n - 1) & 1, &s.abort_flag, vstatus))
         break;
       mbar_arrive_expect_tx(&s.v_full[st], kChunks * Smem::kChunkBytes);
       for (int c = 0; c < kChunks; ++c)
-        tma_load_3d(s.v[st][c], &tm_v, &s.v_full[st], c * 64, g.kv_tm ? b * g.Hkv + hk : (kt_lo + j) * kTile, g.kv_tm ? (kt_lo + j) * kTile : b * g.Hkv + hk);
+        tma_load_3d(s.v[st][c], &tm_v, &s.v_full[st], c * 64, g.kv_tm ? b * g.Hkv + hk : tile_of(j) * kTile, g.kv_tm ? tile_of(j) * kTile : b * g.Hkv + hk);
       ++v_issued;
     }
     if (v_issued < nk) {
@@ -279,18 +290,20 @@ __global__ void __launch_bounds__(128 + NQ * 128, 1)
     const int i = qt * kTile + r;
     const bool real = i < n_real;
     int jlo = 1, jhi = 0;  // allowed K/V buffer rows [jlo, jhi] of this row
+    int slo = 1, shi = 0;  // kSink: and its document's sinks [slo, shi] before them
     if (real) {
       const int p = g.row_offset + i;
       const int doc_start = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + i];
       jlo = row_lo_window(doc_start, p, g.window) - g.kv_offset;
       jhi = min(p - g.kv_offset, g.S_kv - 1);  // a K/V chunk may end before the row
+      if constexpr (kSink) sink_interval(g, doc_start, &jlo, &slo, &shi);
     }
     const float sl2 = g.scale * 1.4426950408889634f;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < nk; ++j) {
       uint32_t km[4];  // dropout: keep bits of this row over the tile's 128 keys
-      if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + (kt_lo + j) * kTile, km);
+      if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + tile_of(j) * kTile, km);
       if (!warp_wait(&s.s_full[qi], j & 1, &s.abort_flag, vstatus)) {
         ok = false;
         break;
@@ -305,13 +318,27 @@ __global__ void __launch_bounds__(128 + NQ * 128, 1)
       tmem_regs_ready<64>(&xr[0]);
       tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&xr[64]));
       tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&xr[96]));
-      const int c0 = (kt_lo + j) * kTile;
+      const int c0 = tile_of(j) * kTile;
       // a row either sees the whole tile, none of it (another document, or a
       // padding row), or part of it (the diagonal / document-start tiles); only
       // a warp with a partly seen row needs the per-element mask
-      const bool dead = jhi < c0 || jlo > c0 + kTile - 1;
-      const bool unmasked = __all_sync(0xffffffffu, dead || (jlo <= c0 && c0 + kTile - 1 <= jhi));
-      const int a_lo = jlo - c0, e_hi = jhi - c0;
+      // (kSink: a row sees the tile through its window or its sinks; both at
+      // once only where the sinks end in the window's first tile)
+      int wlo = jlo, whi = jhi;
+      bool both = false;
+      if constexpr (kSink) {
+        if (shi >= c0 && slo <= c0 + kTile - 1 && slo <= shi) {
+          both = !(jhi < c0 || jlo > c0 + kTile - 1);
+          if (!both) {
+            wlo = slo;
+            whi = shi;
+          }
+        }
+        both = __any_sync(0xffffffffu, both);
+      }
+      const bool dead = whi < c0 || wlo > c0 + kTile - 1;
+      const bool unmasked = __all_sync(0xffffffffu, dead || (wlo <= c0 && c0 + kTile - 1 <= whi));
+      const int a_lo = wlo - c0, e_hi = whi - c0;
       float x[128];  // raw scores, -inf where masked
       float mx[8];   // eight independent 16-column maxima (short dependency chains)
 #pragma unroll
@@ -326,6 +353,14 @@ __global__ void __launch_bounds__(128 + NQ * 128, 1)
         } else {
 #pragma unroll
           for (int c = 64 * hf; c < 64 * hf + 64; ++c) x[c] = (c >= a_lo && c <= e_hi) ? __uint_as_float(xr[c]) : -INFINITY;
+          if constexpr (kSink) {
+            if (both) {
+              const int b_lo = slo - c0, b_hi = shi - c0;
+#pragma unroll
+              for (int c = 64 * hf; c < 64 * hf + 64; ++c)
+                if (c >= b_lo && c <= b_hi) x[c] = __uint_as_float(xr[c]);
+            }
+          }
         }
 #pragma unroll
         for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
@@ -513,8 +548,13 @@ static cudaError_t launch_one(const CUtensorMap& mq, const CUtensorMap& mk, cons
                               const int32_t* seg, const Geom& g, __nv_bfloat16* out, float* lse, int32_t* status,
                               int merge, cudaStream_t st) {
   const size_t smem = sizeof(FwdSmem<D, NQ, NS>) + 1024;  // + 1 KB to align the swizzled tiles
-  auto kern = g.drop_t ? (merge ? fwd_kernel<D, NQ, NS, true, true> : fwd_kernel<D, NQ, NS, false, true>)
-                       : (merge ? fwd_kernel<D, NQ, NS, true, false> : fwd_kernel<D, NQ, NS, false, false>);
+  auto kern =
+      g.n_sink
+          ? (g.drop_t ? (merge ? fwd_kernel<D, NQ, NS, true, true, true> : fwd_kernel<D, NQ, NS, false, true, true>)
+                      : (merge ? fwd_kernel<D, NQ, NS, true, false, true> : fwd_kernel<D, NQ, NS, false, false, true>))
+          : (g.drop_t ? (merge ? fwd_kernel<D, NQ, NS, true, true, false> : fwd_kernel<D, NQ, NS, false, true, false>)
+                      : (merge ? fwd_kernel<D, NQ, NS, true, false, false>
+                               : fwd_kernel<D, NQ, NS, false, false, false>));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(g.B) * g.nqt * (g.Hq / NQ);

@@ -70,6 +70,69 @@ __device__ int block_exclusive_scan(int v, int* s_red, int* total) {
 
 }  // namespace
 
+// The sink-only rows of K/V tile kt of batch row b (local rows [sb, se), none
+// if sb >= se) and the tile row rbase from which its sinks with such rows start.
+// A superset: the kernels mask pair by pair.
+__device__ void sink_tile_rows(const Geom& g, const int32_t* seg, int b, int kt, int* sb, int* se, int* rbase) {
+  *sb = *se = *rbase = 0;
+  if (g.window <= 0 || g.n_sink <= 0) return;
+  const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
+  const int32_t* cu_q = seg + g.off[BD_SEG_OFF_CU_Q] + b * (g.L + 1);
+  const int ro = g.row_offset, n_seg = hdr[BD_SEG_N_SEG], s_first = hdr[BD_SEG_S_FIRST];
+  if (n_seg <= 0) return;
+  const int s_lo = g.kv_offset + kt * kTile;
+  const int s_hi = g.kv_offset + min(kt * kTile + kTile - 1, g.S_kv - 1);
+  const int k_lo = max(s_lo, s_first), k_hi = min(s_hi, hdr[BD_SEG_REAL_END] - 1);
+  if (k_hi < k_lo) return;
+  // the document [ds, de) of the tile's last key
+  int k = 0;
+  if (k_hi >= ro) {
+    int a = 0, e = n_seg - 1;
+    while (a < e) {
+      const int mid = (a + e + 1) >> 1;
+      if (ro + cu_q[mid] <= k_hi) a = mid; else e = mid - 1;
+    }
+    k = a;
+  }
+  const int ds = k == 0 ? s_first : ro + cu_q[k], de = ro + cu_q[k + 1];
+  const int first = max(ds, k_lo);  // its first key in the tile
+  int beg = 0x3fffffff, end = 0;
+  if (first - ds < g.n_sink) {
+    beg = max(0, first + g.window - ro);
+    end = de - ro;
+  }
+  *rbase = first - s_lo;
+  if (g.window < kTile) {  // earlier documents of the tile may have such rows inside it
+    if (ds > k_lo) {
+      const int beg2 = max(0, k_lo + g.window - ro), end2 = ds - ro;
+      if (beg2 < end2) {
+        beg = min(beg, beg2);
+        end = max(end, end2);
+      }
+    }
+    *rbase = 0;
+  }
+  if (beg < end) {
+    *sb = beg;
+    *se = end;
+  }
+}
+
+// The local rows with a window pair in K/V tile kt: [*wb, *we).
+__device__ void window_tile_rows(const Geom& g, const int32_t* rowlo, int n_real, int kt, int* wb, int* we) {
+  const int s_lo = g.kv_offset + kt * kTile;
+  const int s_hi = g.kv_offset + min(kt * kTile + kTile - 1, g.S_kv - 1);
+  const int i_begin = max(0, s_lo - g.row_offset);
+  // first row in [i_begin, n_real) whose lo exceeds s_hi
+  int a = i_begin, e = n_real;
+  while (a < e) {
+    const int mid = (a + e) >> 1;
+    if (row_lo_window(rowlo[mid], g.row_offset + mid, g.window) > s_hi) e = mid; else a = mid + 1;
+  }
+  *wb = i_begin < a ? i_begin : 0;
+  *we = i_begin < a ? a : 0;
+}
+
 // One CTA per batch row.
 __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restrict__ doc, Geom g,
                                                          int32_t* __restrict__ seg, int32_t* status, int kv_chunk) {
@@ -196,7 +259,8 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
 
   if (tid == 0) {
     cu_k[n_seg] = real_end - s_first;
-    const int need_lo = n_real > 0 ? row_lo_window(s_first, ro, g.window) : ro;
+    // the first row's sinks are needed too (a no-op without a window)
+    const int need_lo = n_real == 0 ? ro : g.n_sink > 0 ? s_first : row_lo_window(s_first, ro, g.window);
     // a chunk of the K/V range need not hold every key the rows may attend
     const int kv_bad = !kv_chunk && n_real > 0 && (need_lo < g.kv_offset || real_end > g.kv_offset + g.S_kv);
     const int row_status = (bad ? BD_STATUS_LAYOUT : 0) | (kv_bad ? BD_STATUS_KV_RANGE : 0);
@@ -220,7 +284,9 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
     hdr[kHdrSfull] = g.S_full;
     hdr[kHdrKvChunk] = kv_chunk;
     hdr[kHdrMagic] = kSegMagic;
-    for (int x = kHdrKvChunk + 1; x < BD_SEG_HDR_WORDS; ++x) hdr[x] = 0;
+    hdr[kHdrSink] = g.n_sink;
+    hdr[kHdrSinkTab] = g.sink_tab;
+    for (int x = kHdrSinkTab + 1; x < BD_SEG_HDR_WORDS; ++x) hdr[x] = 0;
     if (row_status) atomicOr(status, row_status);
   }
 }
@@ -285,19 +351,18 @@ __global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restr
 
     // Per K/V tile: the local q rows whose allowed interval meets it.
     for (int kt = tid; kt < g.nkt; kt += nthr) {
-      const int s_lo = g.kv_offset + kt * kTile;
-      const int s_hi = g.kv_offset + min(kt * kTile + kTile - 1, g.S_kv - 1);
-      const int i_begin = max(0, s_lo - ro);
-      // first row in [i_begin, n_real) whose lo exceeds s_hi
-      int a = i_begin, e = n_real;
-      while (a < e) {
-        const int mid = (a + e) >> 1;
-        if (row_lo_window(rowlo[mid], ro + mid, W) > s_hi) e = mid; else a = mid + 1;
+      int wb, we, sb, se, rbase;
+      window_tile_rows(g, rowlo, n_real, kt, &wb, &we);
+      if (g.n_sink > 0) {
+        sink_tile_rows(g, seg, b, kt, &sb, &se, &rbase);
+        if (sb < se) {
+          wb = wb < we ? min(wb, sb) : sb;
+          we = max(we, se);
+        }
       }
-      const int i_end = a;
-      kq[2 * kt] = (i_begin < i_end) ? i_begin : 0;
-      kq[2 * kt + 1] = (i_begin < i_end) ? i_end : 0;
-      n_kv_att += i_begin < i_end ? 1 : 0;
+      kq[2 * kt] = wb;
+      kq[2 * kt + 1] = we;
+      n_kv_att += wb < we ? 1 : 0;
     }
   }
   n_full = block_reduce(n_full, AddOp(), s_red);
@@ -324,6 +389,13 @@ __global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restr
       if (list == 0) {
         const int32_t* qk = seg + g.off[BD_SEG_OFF_QT_KRANGE] + item * 2;
         key = qk[1] >= qk[0] ? qk[1] - qk[0] + 1 : 0;
+        if (g.n_sink > 0) {
+          const int b = item / g.nqt;
+          int x0, nx;
+          sink_extra_tiles(g, seg, b, item % g.nqt, seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL],
+                           qk[0], key, &x0, &nx);
+          key += nx;
+        }
       } else {
         const int32_t* kq = seg + g.off[BD_SEG_OFF_KT_QRANGE] + item * 2;
         key = kq[1] > kq[0] ? (kq[1] - 1) / kBwdQ - kq[0] / kBwdQ + 1 : 0;
@@ -352,6 +424,114 @@ __global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restr
   }
 }
 
+// The backward's units of a sink table (one CTA): every K/V tile's window rows
+// as one unit and its sink-only rows in units of sk_split q tiles, listed
+// longest first; partial slots numbered in tile order, so the order in which
+// the last kernel adds them does not depend on the run. Dynamic shared memory:
+// nbins ints of histogram.
+__global__ void __launch_bounds__(1024) sink_units_kernel(Geom g, int32_t* __restrict__ seg, int nbins,
+                                                          int32_t* status) {
+  pdl_begin();
+  extern __shared__ int s_hist[];
+  __shared__ int s_red[32];
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  int32_t* hdr = seg + g.sk_off;
+  int32_t* units = hdr + kSinkHdrWords;
+  int32_t* sums = units + static_cast<size_t>(g.sk_units) * kSinkUnitWords;
+  const int n_items = g.B * g.nkt, span = g.sk_split * kTile;
+  auto bin_of = [&](int beg, int end) { return nbins - 1 - min((end - 1) / kBwdQ - beg / kBwdQ + 1, nbins - 1); };
+  // unit x of a tile with window rows [wb, we) and sink-only rows [sb, se)
+  auto unit_range = [&](int x, int wb, int we, int sb, int se, int* beg, int* end, int* sink) {
+    const int has_w = wb < we;
+    if (has_w && x == 0) {
+      *beg = wb;
+      *end = we;
+      *sink = 0;
+      return;
+    }
+    const int first = (sb / kTile) * kTile, y = x - has_w;
+    *beg = max(sb, first + y * span);
+    *end = min(se, first + (y + 1) * span);
+    *sink = 1;
+  };
+  auto ranges = [&](int item, int* wb, int* we, int* sb, int* se, int* rbase) -> int {
+    const int b = item / g.nkt, kt = item % g.nkt;
+    const int n_real = seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL];
+    window_tile_rows(g, seg + g.off[BD_SEG_OFF_ROW_LO] + b * g.L, n_real, kt, wb, we);
+    sink_tile_rows(g, seg, b, kt, sb, se, rbase);
+    const int n_s = *sb < *se ? cdiv(*se - (*sb / kTile) * kTile, span) : 0;
+    return (*wb < *we ? 1 : 0) + n_s;
+  };
+  for (int x = tid; x < nbins; x += nthr) s_hist[x] = 0;
+  __syncthreads();
+  int n_units = 0;
+  for (int item = tid; item < n_items; item += nthr) {
+    int wb, we, sb, se, rbase, beg, end, sink;
+    const int n = ranges(item, &wb, &we, &sb, &se, &rbase);
+    for (int x = 0; x < n; ++x) {
+      unit_range(x, wb, we, sb, se, &beg, &end, &sink);
+      atomicAdd(&s_hist[bin_of(beg, end)], 1);
+    }
+    n_units += n;
+  }
+  n_units = block_reduce(n_units, AddOp(), s_red);
+  int carry = 0;  // exclusive scan of the histogram, in chunks of blockDim
+  for (int c0 = 0; c0 < nbins; c0 += nthr) {
+    const int x = c0 + tid;
+    const int v = x < nbins ? s_hist[x] : 0;
+    int tot;
+    const int ex = block_exclusive_scan(v, s_red, &tot);
+    __syncthreads();
+    if (x < nbins) s_hist[x] = carry + ex;
+    carry += tot;
+    __syncthreads();
+  }
+  int n_sums = 0, n_slots = 0;
+  bool over = n_units > g.sk_units;
+  for (int c0 = 0; c0 < n_items; c0 += nthr) {
+    const int item = c0 + tid;
+    int wb = 0, we = 0, sb = 0, se = 0, rbase = 0, n = 0;
+    if (item < n_items) n = ranges(item, &wb, &we, &sb, &se, &rbase);
+    const int multi = n > 1;
+    int tot_sums, tot_slots;
+    const int sum = n_sums + block_exclusive_scan(multi, s_red, &tot_sums);
+    const int slot0 = n_slots + block_exclusive_scan(multi ? n : 0, s_red, &tot_slots);
+    if (multi && (sum >= g.sk_sums || slot0 + n > g.sk_slots)) over = true;
+    if (multi && sum < g.sk_sums) {
+      int32_t* e = sums + static_cast<size_t>(sum) * kSinkSumWords;
+      e[0] = item;
+      e[1] = slot0;
+      e[2] = n;
+      e[3] = rbase;
+    }
+    for (int x = 0; x < n; ++x) {
+      int beg, end, sink;
+      unit_range(x, wb, we, sb, se, &beg, &end, &sink);
+      const int pos = atomicAdd(&s_hist[bin_of(beg, end)], 1);
+      if (pos >= g.sk_units) continue;
+      int32_t* u = units + static_cast<size_t>(pos) * kSinkUnitWords;
+      u[0] = item;
+      u[1] = beg;
+      u[2] = end;
+      u[3] = (sink ? kUnitSink : 0) | (x == 0 ? kUnitPrimary : 0);
+      u[4] = multi ? slot0 + x : -1;
+      u[5] = rbase;
+      u[6] = u[7] = 0;
+    }
+    n_sums += tot_sums;
+    n_slots += tot_slots;
+  }
+  over = block_reduce(over ? 1 : 0, OrOp(), s_red) != 0;
+  if (tid == 0) {
+    // an overflow would be an error of the capacities: nothing is run on the table
+    hdr[0] = over ? -1 : n_units;
+    hdr[1] = over ? -1 : n_sums;
+    hdr[2] = n_slots;
+    for (int x = 3; x < kSinkHdrWords; ++x) hdr[x] = 0;
+    if (over) atomicOr(status, BD_STATUS_BOUNDS);
+  }
+}
+
 cudaError_t launch_seg_build(const int32_t* doc, const Geom& g, int32_t* seg, int32_t* status, cudaStream_t st,
                              int kv_chunk) {
   if (const cudaError_t le = launch_pdl(seg_build_kernel, dim3(g.B), dim3(1024), 0, st, doc, g, seg, status, kv_chunk);
@@ -363,6 +543,10 @@ cudaError_t launch_seg_build(const int32_t* doc, const Geom& g, int32_t* seg, in
   if (nbins > 12288) nbins = 12288;
   if (const cudaError_t le = launch_pdl(classify_kernel, dim3(1), dim3(1024), static_cast<size_t>(nbins) * 4, st, g,
       seg, nbins); le != cudaSuccess) return le;
+  if (g.sink_tab) {
+    if (const cudaError_t le = launch_pdl(sink_units_kernel, dim3(1), dim3(1024), static_cast<size_t>(nbins) * 4, st, g,
+        seg, nbins, status); le != cudaSuccess) return le;
+  }
   return cudaGetLastError();
 }
 
