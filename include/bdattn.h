@@ -363,6 +363,58 @@ int bd_attn_sink_bwd_main(const void* dout, const void* q, const void* k, const 
                           const void* seg, const bd_geom* g, int n_sink, int grad_dtype, void* dk, void* dv,
                           void* workspace, int32_t* status, bd_stream_t stream);
 
+/* ---- paged K/V cache: append and decode -----------------------------------
+ *
+ * Serving keeps the keys and values of running sequences in pages:
+ *   k_pages, v_pages  bf16  [n_pages, Hkv, page_size, D]
+ *   page_table        int32 [B, max_pages]  page of a sequence's tokens
+ *                           [i * page_size, (i + 1) * page_size); -1: none
+ *   seq_lens          int32 [B]  tokens of each sequence, the new ones included
+ * page_size is any number >= 1; B <= 65536, B * Hq <= 2^22, max_pages *
+ * page_size <= 2^30, n_pages * Hkv * page_size < 2^31 (else BD_ERR_ARG). Data
+ * pointers are 16-byte aligned, everything else as above: caller-owned, one
+ * stream, no allocation, no synchronisation, nothing done once *status is set.
+ * Page ids, lengths and offsets are read on the device and checked there: one
+ * out of range sets BD_STATUS_BOUNDS and its token is neither read nor written
+ * (what a call returns is then not to be used). */
+typedef struct {
+  int B;          /* sequences (places of the batch) */
+  int Hq;         /* query heads (append: any multiple of Hkv) */
+  int Hkv;        /* key/value heads; Hq % Hkv == 0 */
+  int D;          /* head dim: 64, 128, 256 or 512 */
+  int n_pages;    /* pages of the cache */
+  int page_size;  /* tokens per page */
+  int max_pages;  /* row length of page_table */
+  int window;     /* left window W (> 0: also require p - s < W); <= 0: none */
+  int n_sink;     /* >= 0; with a window, the first tokens that stay visible */
+  float scale;    /* softmax scale; <= 0 means D^-0.5 */
+} bd_paged;
+
+/* Write new tokens into their sequences' pages. k_new, v_new: bf16
+ * [n_tokens, Hkv, D], sequence after sequence: sequence b's are
+ * [cu_new[b], cu_new[b+1]) (int32 [B+1], cu_new[0] = 0, cu_new[B] <= n_tokens)
+ * and its last one goes to position seq_lens[b] - 1. Rows from cu_new[B] on are
+ * padding. A token whose page is -1 is dropped (with a window, a long prompt's
+ * tokens that no later token sees need no page). No two tokens may share a
+ * place in the cache. */
+int bd_attn_paged_append(const void* k_new, const void* v_new, const int32_t* cu_new, const int32_t* seq_lens,
+                         const int32_t* page_table, const bd_paged* g, int n_tokens, void* k_pages, void* v_pages,
+                         int32_t* status, bd_stream_t stream);
+
+/* Attention of one new token per sequence, q bf16 [B, Hq, D], at position
+ * seq_lens[b] - 1, over its sequence's cached keys (its own among them):
+ * out bf16 [B, Hq, D] and lse fp32 [B, Hq] (natural log), the rule of
+ * bd_attn_sink_fwd. Only visible tokens' pages are read: behind the window the
+ * table may hold anything, and a page's places behind the sequence may too. A
+ * sequence of length 0 gets out = 0, lse = -inf. Results are bitwise
+ * reproducible for the same lengths. workspace:
+ * bd_attn_paged_decode_workspace_bytes bytes, 16-byte aligned, not shared by
+ * calls that may overlap. */
+size_t bd_attn_paged_decode_workspace_bytes(const bd_paged* g);
+int bd_attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                         const int32_t* seq_lens, const bd_paged* g, void* out, float* lse, void* workspace,
+                         int32_t* status, bd_stream_t stream);
+
 /* ---- K/V exchange plans (blockdiag_cp.exchange) --------------------------
  *
  * The global left-halo plan and the needed-only all-to-all-v split plan,

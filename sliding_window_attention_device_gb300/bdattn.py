@@ -41,7 +41,8 @@ EXPORTS = ("bd_attn_seg_bytes", "bd_attn_seg_layout", "bd_attn_seg_build", "bd_a
            "bd_attn_needed_gather", "bd_attn_needed_scatter_add", "bd_attn_strerror",
            "bd_attn_sink_seg_bytes", "bd_attn_sink_seg_build", "bd_attn_sink_fwd", "bd_attn_sink_fwd_merge",
            "bd_attn_sink_bwd_workspace_bytes", "bd_attn_sink_bwd", "bd_attn_sink_bwd_deterministic",
-           "bd_attn_sink_bwd_main",
+           "bd_attn_sink_bwd_main", "bd_attn_paged_append", "bd_attn_paged_decode_workspace_bytes",
+           "bd_attn_paged_decode",
            "bd_attn_selftest_wait_timeout")
 
 # exchange plan: header fields (BD_PLAN_*) and regions (BD_PLAN_OFF_*)
@@ -61,6 +62,15 @@ class Geom(ctypes.Structure):
 
     def __repr__(self):
         return "Geom(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("window", ctypes.c_int), ("n_sink", ctypes.c_int), ("scale", ctypes.c_float)]
+
+    def __repr__(self):
+        return "Paged(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
 KV_BHSD, KV_SBHD = 0, 1  # K/V layouts: [B, Hkv, S_kv, D] or token-major [S_kv, B, Hkv, D]
@@ -152,6 +162,13 @@ def load() -> ctypes.CDLL:
         lib.bd_attn_sink_bwd_main.argtypes = [P, P, P, P, P, P, G, I, I, P, P, P, P, P]
         for name in ("seg_build", "fwd", "fwd_merge", "bwd", "bwd_deterministic", "bwd_main"):
             getattr(lib, "bd_attn_sink_" + name).restype = I
+        PG = ctypes.POINTER(Paged)
+        lib.bd_attn_paged_append.argtypes = [P, P, P, P, P, PG, I, P, P, P, P]
+        lib.bd_attn_paged_append.restype = I
+        lib.bd_attn_paged_decode_workspace_bytes.argtypes = [PG]
+        lib.bd_attn_paged_decode_workspace_bytes.restype = ctypes.c_size_t
+        lib.bd_attn_paged_decode.argtypes = [P, P, P, P, P, PG, P, P, P, P, P]
+        lib.bd_attn_paged_decode.restype = I
         lib.bd_attn_strerror.argtypes = [ctypes.c_int]
         lib.bd_attn_strerror.restype = ctypes.c_char_p
         lib.bd_attn_selftest_wait_timeout.argtypes = [P, ctypes.c_uint64, P]
@@ -599,6 +616,73 @@ def bd_attn_sink_bwd_main(dout, q, k, v, lse, seg, g: Geom, n_sink: int, status,
         _check(load().bd_attn_sink_bwd_main(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(lse), _ptr(seg),
                                             ctypes.byref(g), int(n_sink), code, _ptr(dk), _ptr(dv), _ptr(workspace),
                                             _ptr(status), st), "bd_attn_sink_bwd_main")
+
+
+# ------------------------------------------------------------ paged K/V cache
+def paged_geom(B, Hq, Hkv, D, n_pages, page_size, max_pages, window=0, n_sink=0, scale=0.0) -> Paged:
+    """Geometry of a paged cache [n_pages, Hkv, page_size, D] and the B sequences
+    in it (page table [B, max_pages]); window <= 0: none; n_sink: first tokens
+    that stay visible past the window; scale <= 0 means D**-0.5."""
+    return Paged(int(B), int(Hq), int(Hkv), int(D), int(n_pages), int(page_size), int(max_pages), int(window),
+                 int(n_sink), float(scale or 0.0))
+
+
+def paged_decode_workspace_bytes(pg: Paged) -> int:
+    n = load().bd_attn_paged_decode_workspace_bytes(ctypes.byref(pg))
+    if n == 0:
+        raise ValueError(f"invalid geometry {pg}")
+    return int(n)
+
+
+def _need_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev):
+    shape = (pg.n_pages, pg.Hkv, pg.page_size, pg.D)
+    _need(k_pages, "k_pages", torch.bfloat16, shape, dev)
+    _need(v_pages, "v_pages", torch.bfloat16, shape, dev)
+    _need(page_table, "page_table", torch.int32, (pg.B, pg.max_pages), dev)
+    _need(seq_lens, "seq_lens", torch.int32, (pg.B,), dev)
+    _need(status, "status", torch.int32, (1,), dev)
+
+
+def bd_attn_paged_append(k_new, v_new, cu_new, seq_lens, page_table, pg: Paged, k_pages, v_pages, status,
+                         stream=None):
+    """Write k_new, v_new [T, Hkv, D] (sequence b's tokens at [cu_new[b], cu_new[b+1]), the last one at position
+    seq_lens[b] - 1) into k_pages, v_pages in place."""
+    dev = _cuda_device(k_pages, "k_pages")
+    _need_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev)
+    n = _cuda_device(k_new, "k_new") and k_new.shape[0]
+    _need(k_new, "k_new", torch.bfloat16, (n, pg.Hkv, pg.D), dev)
+    _need(v_new, "v_new", torch.bfloat16, (n, pg.Hkv, pg.D), dev)
+    _need(cu_new, "cu_new", torch.int32, (pg.B + 1,), dev)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        _check(load().bd_attn_paged_append(_ptr(k_new), _ptr(v_new), _ptr(cu_new), _ptr(seq_lens), _ptr(page_table),
+                                           ctypes.byref(pg), int(n), _ptr(k_pages), _ptr(v_pages), _ptr(status), st),
+               "bd_attn_paged_append")
+
+
+def bd_attn_paged_decode(q, k_pages, v_pages, page_table, seq_lens, pg: Paged, status, out=None, lse=None,
+                         workspace=None, stream=None):
+    """out [B, Hq, D] bf16 and lse [B, Hq] fp32 of one new token per sequence (q [B, Hq, D], at position
+    seq_lens[b] - 1) over its cached keys; out 0 and lse -inf for a sequence of length 0."""
+    dev = _cuda_device(q, "q")
+    _need(q, "q", torch.bfloat16, (pg.B, pg.Hq, pg.D), dev)
+    _need_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev)
+    n = paged_decode_workspace_bytes(pg)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(pg.B, pg.Hq, pg.D, dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty(pg.B, pg.Hq, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        _need(out, "out", torch.bfloat16, (pg.B, pg.Hq, pg.D), dev)
+        _need(lse, "lse", torch.float32, (pg.B, pg.Hq), dev)
+        _need(workspace, "workspace", torch.uint8, (n,), dev)
+        _check(load().bd_attn_paged_decode(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(seq_lens),
+                                           ctypes.byref(pg), _ptr(out), _ptr(lse), _ptr(workspace), _ptr(status), st),
+               "bd_attn_paged_decode")
+    return out, lse
 
 
 # ------------------------------------------------------------ exchange plans

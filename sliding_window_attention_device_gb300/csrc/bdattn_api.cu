@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "paged.cuh"
 #include "sm100_ptx.cuh"
 
 namespace bd {
@@ -44,6 +45,13 @@ cudaError_t launch_needed_gather(const void* x, const int32_t* plan, int B, int 
 cudaError_t launch_needed_scatter_add(const void* gsend, const int32_t* plan, int B, int C, int L, int vshift,
                                       int bf16, void* glocal, int max_rows, int32_t* status, cudaStream_t st);
 int bwd_q_box_rows(int D);
+cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int32_t* cu_new, const int32_t* seq_lens,
+                                const int32_t* page_table, const PagedGeom& g, int n_tokens, void* k_pages,
+                                void* v_pages, int32_t* status, cudaStream_t st);
+size_t paged_decode_workspace_bytes(const PagedGeom& g);
+cudaError_t launch_paged_decode(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                                const int32_t* seq_lens, const PagedGeom& g, void* out, float* lse, void* workspace,
+                                int32_t* status, cudaStream_t st);
 cudaError_t launch_sink_sum(const int32_t* seg, const Geom& g, void* dk, void* dv, int bf16, int32_t* status,
                             cudaStream_t st);
 
@@ -621,6 +629,74 @@ int bd_attn_bwd_noalloc(const void* dout, const void* q, const void* k, const vo
   if (int rc = noalloc_scratch(&scratch)) return rc;
   // same three stages as bd_attn_bwd; the prep stage zeroes the accumulator
   return bd_attn_bwd(dout, q, k, v, out, lse, seg, gi, grad_dtype, dq, dk, dv, scratch, status, stream);
+}
+
+// ---------------------------------------------------------- paged K/V cache
+}  // extern "C"
+
+namespace {
+int to_paged(const bd_paged* in, PagedGeom* g) {
+  if (!in) return BD_ERR_ARG;
+  if (in->B < 1 || in->Hq < 1 || in->Hkv < 1 || in->Hq % in->Hkv != 0) return BD_ERR_ARG;
+  if (in->D != 64 && in->D != 128 && in->D != 256 && in->D != 512) return BD_ERR_ARG;
+  if (in->n_pages < 1 || in->page_size < 1 || in->max_pages < 1 || in->n_sink < 0) return BD_ERR_ARG;
+  // positions and cache rows stay within 32 bits
+  if (in->B > (1 << 16) || static_cast<long long>(in->B) * in->Hq > (1 << 22)) return BD_ERR_ARG;
+  if (static_cast<long long>(in->max_pages) * in->page_size > (1LL << 30)) return BD_ERR_ARG;
+  const long long tokens = static_cast<long long>(in->n_pages) * in->page_size;
+  if (tokens > 0x7fffffffLL || tokens * in->Hkv > 0x7fffffffLL) return BD_ERR_ARG;
+  if (!(in->scale == in->scale)) return BD_ERR_ARG;  // NaN
+  g->B = in->B;
+  g->Hq = in->Hq;
+  g->Hkv = in->Hkv;
+  g->D = in->D;
+  g->G = in->Hq / in->Hkv;
+  g->n_pages = in->n_pages;
+  g->page_size = in->page_size;
+  g->max_pages = in->max_pages;
+  g->page_shift = -1;
+  for (int x = 0; x < 31; ++x)
+    if (in->page_size == (1 << x)) g->page_shift = x;
+  g->window = in->window > 0 ? in->window : 0;
+  g->n_sink = g->window > 0 ? in->n_sink : 0;  // without a window every earlier key is visible anyway
+  g->scale = in->scale > 0.f ? in->scale : 1.0f / std::sqrt(static_cast<float>(in->D));
+  return BD_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int bd_attn_paged_append(const void* k_new, const void* v_new, const int32_t* cu_new, const int32_t* seq_lens,
+                         const int32_t* page_table, const bd_paged* gi, int n_tokens, void* k_pages, void* v_pages,
+                         int32_t* status, bd_stream_t stream) {
+  PagedGeom g;
+  if (int rc = to_paged(gi, &g)) return rc;
+  if (!cu_new || !seq_lens || !page_table || !k_pages || !v_pages || !status) return BD_ERR_ARG;
+  if (n_tokens < 0 || (n_tokens > 0 && (!k_new || !v_new))) return BD_ERR_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages)) return BD_ERR_ARG;
+  if (int rc = check_device()) return rc;
+  return cuda_rc(launch_paged_append(k_new, v_new, cu_new, seq_lens, page_table, g, n_tokens, k_pages, v_pages, status,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t bd_attn_paged_decode_workspace_bytes(const bd_paged* gi) {
+  PagedGeom g;
+  if (to_paged(gi, &g) != BD_OK) return 0;
+  return paged_decode_workspace_bytes(g);
+}
+
+int bd_attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                         const int32_t* seq_lens, const bd_paged* gi, void* out, float* lse, void* workspace,
+                         int32_t* status, bd_stream_t stream) {
+  PagedGeom g;
+  if (int rc = to_paged(gi, &g)) return rc;
+  if (!q || !k_pages || !v_pages || !page_table || !seq_lens || !out || !lse || !workspace || !status)
+    return BD_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))
+    return BD_ERR_ARG;
+  if (int rc = check_device()) return rc;
+  return cuda_rc(launch_paged_decode(q, k_pages, v_pages, page_table, seq_lens, g, out, lse, workspace, status,
+                                     static_cast<cudaStream_t>(stream)));
 }
 
 const char* bd_attn_strerror(int code) {
