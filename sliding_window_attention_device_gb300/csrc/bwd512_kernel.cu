@@ -71,7 +71,7 @@ struct Bwd512Smem {
   uint32_t tmem_base;
   int abort_flag;
   int b, kt, q64_lo, nq64, n_real, skip, work, n_att;
-  int u_flags, u_slot, u_rbase;  // kSink: the unit's flags, partial slot and first partial row
+  int u_primary, u_slot, u_rbase;  // kSink: the unit's kind, partial slot and first partial row
 };
 
 __device__ __forceinline__ void red_add_f32(float* addr, float v) {
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads5, 1)
     const int32_t* qr = seg + g.off[BD_SEG_OFF_KT_QRANGE] + (b * g.nkt + kt) * 2;
     const int qlo = kSink ? u[1] : qr[0], qhi = kSink ? u[2] : qr[1];
     if constexpr (kSink) {
-      s.u_flags = u[3];
+      s.u_primary = u[3];
       s.u_slot = u[4];
       s.u_rbase = u[5];
       ok = ok && u[4] < g.sk_slots && u[5] >= 0 && u[5] < kTile;
@@ -409,9 +409,8 @@ __global__ void __launch_bounds__(kThreads5, 1)
         if constexpr (kSink) doc_beg = k == 0 ? hdr[BD_SEG_S_FIRST] : g.row_offset + cu_q[k];
       }
     }
-    int row_beg = key, row_end = min(doc_end, g.window > 0 ? key + g.window : 0x3fffffff);
-    if constexpr (kSink)  // in this unit
-      unit_rows(g, key, doc_beg, doc_end, (s.u_flags & kUnitSink) != 0, &row_beg, &row_end);
+    int row_end = min(doc_end, g.window > 0 ? key + g.window : 0x3fffffff);
+    if constexpr (kSink) row_end = sink_row_end(g, key, doc_beg, doc_end);
     // dropout: scale * keep scale multiplies a kept dP (a dropped one is zero)
     const float sc_dp = kDrop ? g.scale * g.drop_scale : g.scale;
     bool ok = true;
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(kThreads5, 1)
       tmem_wait_ld();
       // q columns [c_lo, c_hi) of this tile attend the key (relative to c0)
       const int row0 = g.row_offset + q0;
-      const int c_lo = max(0, row_beg - row0) - c0;
+      const int c_lo = max(0, key - row0) - c0;
       const int c_hi = min(min(kBwdQ, n_real - q0), row_end - row0) - c0;
       float p[32];
       const float4* l4 = reinterpret_cast<const float4*>(s.lse2[st] + c0);
@@ -516,7 +515,7 @@ __global__ void __launch_bounds__(kThreads5, 1)
           uint32_t kk[32];
           tmem_ld32(tbase + lane_off + kColDk + c, kk);
           tmem_wait_ld();
-          const int pr = kSink ? unit_part_row(g, s.u_slot, s.u_flags, s.u_rbase, r) : -1;
+          const int pr = kSink ? unit_part_row(g, s.u_slot, s.u_primary, s.u_rbase, r) : -1;
           if (j < g.S_kv && pr != -2) {
             const size_t off = kv_row(g, b, hk, j) * kD5 + slice * kSlice + c;
             if (kSink && pr >= 0) {  // a row that several units of the tile touch: the unit's partial slot

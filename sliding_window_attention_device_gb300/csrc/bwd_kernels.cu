@@ -160,7 +160,7 @@ struct BwdSmem {
   uint32_t tmem_base;
   int abort_flag;
   int b, kt, q64_lo, nq64, n_real, skip, mode, n_att;
-  int u_flags, u_slot, u_rbase;  // kSink: the unit's flags, partial slot and first partial row
+  int u_primary, u_slot, u_rbase;  // kSink: the unit's kind, partial slot and first partial row
 };
 
 constexpr int kBwdThreads = 512;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int32_t* qr = seg + g.off[BD_SEG_OFF_KT_QRANGE] + (b * g.nkt + kt) * 2;
     const int qlo = kSink ? u[1] : qr[0], qhi = kSink ? u[2] : qr[1];
     if constexpr (kSink) {
-      s.u_flags = u[3];
+      s.u_primary = u[3];
       s.u_slot = u[4];
       s.u_rbase = u[5];
       ok = ok && u[4] < g.sk_slots && u[5] >= 0 && u[5] < kTile;
@@ -513,16 +513,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     const int win_end = g.window > 0 ? key + g.window : 0x3fffffff;
-    int row_beg = key, row_end = min(doc_end, win_end);  // rows [row_beg, row_end) attend this key
-    if constexpr (kSink)  // in this unit
-      unit_rows(g, key, doc_beg, doc_end, (s.u_flags & kUnitSink) != 0, &row_beg, &row_end);
+    int row_end = min(doc_end, win_end);  // rows [key, row_end) attend this key
+    if constexpr (kSink) row_end = sink_row_end(g, key, doc_beg, doc_end);
     // dropout: scale * keep scale multiplies a kept dP (a dropped one is zero)
     const float sc_dp = kDrop ? g.scale * g.drop_scale : g.scale;
     // 32 columns from `col` of this key's dk (which = 0) or dv (1) row; kSink:
     // rows that several units of the tile touch go to the unit's partial slot
     auto put = [&](int which, void* base, int col, const float* vals32) {
       if constexpr (kSink) {
-        const int pr = unit_part_row(g, s.u_slot, s.u_flags, s.u_rbase, r);
+        const int pr = unit_part_row(g, s.u_slot, s.u_primary, s.u_rbase, r);
         if (pr == -2) return;
         if (pr >= 0) {
           float4* p4 = reinterpret_cast<float4*>(unit_part(g, s.u_slot, hk, which, pr) + col);
@@ -552,7 +551,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tmem_wait_ld();
       // q columns [c_lo, c_hi) of this tile attend the key (relative to c0)
       const int row0 = g.row_offset + q0;
-      const int c_lo = max(0, row_beg - row0) - c0;
+      const int c_lo = max(0, key - row0) - c0;
       const int c_hi = min(min(kBwdQ, n_real - q0), row_end - row0) - c0;
       float p[32];
       const float4* l4 = reinterpret_cast<const float4*>(s.lse2[st] + c0);

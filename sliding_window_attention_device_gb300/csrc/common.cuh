@@ -29,7 +29,7 @@ struct Geom {
   int sk_off;                     // word offset of the sink header (kSinkHdrWords), then the units, then the sums
   int sk_units, sk_sums, sk_slots;  // capacities of the unit list, the sum list and the partial slots
   int sk_rows;                    // key rows of a partial slot
-  int sk_split;                   // 128-row q tiles of a sink unit
+  int sk_split;                   // 128-row q tiles of a unit
   float* sk_part;                 // partial slots of a backward, in the caller's workspace
 };
 
@@ -56,20 +56,19 @@ __host__ __device__ inline void seg_layout(int B, int L, int S_kv, int* off, int
 }
 
 // ---- sink tables -----------------------------------------------------------
-// With a window W and n sink tokens, the visible pairs of a document split into
-// the window pairs (p - s < W) and the sink-only pairs (p - s >= W, s among the
-// document's first n keys). A K/V tile's window rows are a short range; its
-// sink-only rows run to the document's end. The backward therefore works on
-// units: one window unit per K/V tile that has window rows, and the sink-only
-// rows cut into units of sk_split q tiles. A K/V tile with one unit writes its
-// dk / dv directly; the units of a tile with several write the key rows that
-// more than one unit touches, [rbase, rbase + sk_rows), as fp32 partials into
-// slots of the workspace, which a last kernel adds in slot order.
+// A sink's gradient sums over all later rows of its document: with a window W,
+// the rows that attend a K/V tile are a short range, except that a tile that
+// holds sinks is attended to the document's end. The backward therefore works
+// on units, K/V tile by q rows: a tile's first unit (the primary) covers its
+// window rows, or sk_split 128-row q tiles where that is more, and the rows
+// behind it are cut into units of sk_split q tiles. Only sinks of the tile's
+// last document have such rows. A tile with one unit writes its dk / dv
+// directly; the units of a tile with several write those sinks' key rows,
+// [rbase, rbase + sk_rows), as fp32 partials into slots of the workspace, which
+// a last kernel adds in slot order, and the primary writes the other rows.
 constexpr int kSinkHdrWords = 8;   // n_units, n_sums, n_slots
-constexpr int kSinkUnitWords = 8;  // item (b * nkt + kt), q_begin, q_end (local rows), flags, slot (-1: none), rbase
+constexpr int kSinkUnitWords = 8;  // item (b * nkt + kt), q_begin, q_end (local rows), primary, slot (-1: none), rbase
 constexpr int kSinkSumWords = 4;   // item, first slot, slots, rbase
-constexpr int kUnitSink = 1;       // the unit holds the sink-only pairs (else the window pairs)
-constexpr int kUnitPrimary = 2;    // also writes the tile's rows outside [rbase, rbase + sk_rows)
 
 // Row index of (batch row b, kv head hk, K/V buffer row j) in k, v, dk, dv.
 __host__ __device__ inline size_t kv_row(const Geom& g, int b, int hk, int j) {
@@ -110,32 +109,32 @@ __device__ __forceinline__ int row_lo_window(int doc_start, int p, int window) {
   return (window > 0 && p - window + 1 > doc_start) ? p - window + 1 : doc_start;
 }
 
-// Capacities of a sink table and its partial slots. A K/V tile has sink-only
-// rows only if it holds sinks of a document with rows at distance >= W; for
-// W >= kTile these are the straddling document and documents longer than W, at
-// most 1 + L / W of them, each with its sinks (n <= 128) in at most two tiles,
-// and only the last document of a tile has rows behind the tile. For W < kTile
-// any tile may count, and a document's rows may lie within the tile itself.
+// Capacities of a sink table and its partial slots. A tile has several units
+// only if its last document has more than (sk_split - 2) * kTile local rows, so
+// at most L / that many documents count, each with its sinks (n <= 128) in at
+// most two tiles; a document's rows are cut once for each of the two.
 __host__ __device__ inline void sink_sizes(Geom* g) {
   const bool on = g->window > 0 && g->n_sink > 0;
-  g->sk_rows = g->window >= kTile ? (g->n_sink > 0 ? g->n_sink : 1) : kTile;
+  g->sk_rows = g->n_sink > 0 ? g->n_sink : 1;
   const int w_tiles = g->window / kTile + 1;
-  g->sk_split = w_tiles > 4 ? w_tiles : 4;  // a sink unit no longer than a window unit, nor shorter than 4 tiles
-  long long t = 0, u = 0;
+  g->sk_split = w_tiles > 8 ? w_tiles : 8;  // a unit about as long as a window's, and not short
+  long long t = 0, e = 0;
   if (on) {
-    t = g->window >= kTile ? 2LL * (1 + g->L / g->window) : g->nkt;
+    t = 2LL * (g->L / ((g->sk_split - 2) * kTile) + 1);
     if (t > g->nkt) t = g->nkt;
-    u = t + (2LL * g->nqt + 8 * t) / g->sk_split + 2;
+    e = t + 2LL * (g->L / (g->sk_split * kTile)) + 2;
   }
-  // window units: the K/V tiles reachable by position through the window
+  // tiles with a unit: those reachable by position through the window, and the
+  // straddling document's sinks
   const long long hi = static_cast<long long>(g->row_offset) + g->L - 1 - g->kv_offset;
   const long long lo = g->window > 0 ? static_cast<long long>(g->row_offset) - g->window + 1 - g->kv_offset : 0;
   const long long a = lo > 0 ? lo : 0;
-  const long long e = hi < g->S_kv - 1 ? hi : static_cast<long long>(g->S_kv) - 1;
-  const long long reach = e < a ? 0 : e / kTile - a / kTile + 1;
+  const long long z = hi < g->S_kv - 1 ? hi : static_cast<long long>(g->S_kv) - 1;
+  long long reach = (z < a ? 0 : z / kTile - a / kTile + 1) + (on ? 2 : 0);
+  if (reach > g->nkt) reach = g->nkt;
   g->sk_sums = static_cast<int>(g->B * t);
-  g->sk_slots = static_cast<int>(g->B * (u + t));
-  g->sk_units = static_cast<int>(g->B * (reach + u));
+  g->sk_slots = static_cast<int>(g->B * (t + e));
+  g->sk_units = static_cast<int>(g->B * (reach + e));
 }
 
 // Words of the sink regions (each region a multiple of 4 words).
@@ -144,48 +143,65 @@ __host__ __device__ inline long long sink_words(const Geom& g) {
          static_cast<long long>(g.sk_sums) * kSinkSumWords;
 }
 
-// K/V tiles of q tile qt that only its first document's sinks reach: its rows'
-// window ranges start at lo(first row) (tile kt_lo, n_main tiles, both clipped
-// to the buffer); the sinks before that lie in tiles [*x0, *x0 + *nx), all
-// below kt_lo. A document that starts inside the q tile starts behind lo(first
-// row), so its sinks are in the window range already.
-__device__ inline void sink_extra_tiles(const Geom& g, const int32_t* seg, int b, int qt, int n_real, int kt_lo,
-                                        int n_main, int* x0, int* nx) {
-  *x0 = 0;
-  *nx = 0;
+// Sink passes of q tile qt. The rows of a document see its sinks before their
+// window; only the q tile's first document has sinks that its rows' windows have
+// left behind (a document that starts inside the q tile does so behind the first
+// row's window), and those lie in at most two K/V tiles (n <= 128): [*x0, *x0 +
+// *nx). A q tile walks these first, seeing that document's sinks only, then its
+// window's tiles, seeing the window only (and, for W < kTile, the sinks of the
+// documents that start inside it: RowKeys); a tile may come up in both walks.
+// Where a sink
+// tile's sinks fit 32 columns from a 16-column boundary on, col[] is the first of
+// them and the pass works on 32 keys instead of 128, else -1.
+__device__ inline void sink_passes(const Geom& g, const int32_t* seg, int b, int qt, int n_real, int* x0, int* nx,
+                                   int* col) {
+  *x0 = *nx = 0;
+  col[0] = col[1] = -1;
   const int first = qt * kTile;
   if (g.window <= 0 || g.n_sink <= 0 || first >= n_real) return;
-  const int p = g.row_offset + first;
+  const int last = first + kTile - 1 < n_real - 1 ? first + kTile - 1 : n_real - 1;
   const int ds = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + first];
-  const int lo = p - g.window + 1;  // the first document's rows see no window key before it
+  const int lo = g.row_offset + last - g.window + 1;  // no row of the document sees a window key before it
   if (ds < 0 || lo <= ds) return;
   const int a = ds > g.kv_offset ? ds - g.kv_offset : 0;
   int e = (ds + g.n_sink < lo ? ds + g.n_sink : lo) - 1 - g.kv_offset;
   if (e > g.S_kv - 1) e = g.S_kv - 1;
   if (e < a) return;
-  int t1 = e / kTile;
-  if (n_main > 0 && t1 > kt_lo - 1) t1 = kt_lo - 1;
-  const int t0 = a / kTile;
-  if (t1 < t0) return;
-  *x0 = t0;
-  *nx = t1 - t0 + 1;
+  *x0 = a / kTile;
+  *nx = e / kTile - *x0 + 1;
+  for (int k = 0; k < *nx; ++k) {
+    const int c_a = k == 0 ? a % kTile : 0, c_e = k == *nx - 1 ? e % kTile : kTile - 1;
+    const int c0 = (c_a & ~15) < kTile - 32 ? (c_a & ~15) : kTile - 32;
+    if (c_e - c0 < 32) col[k] = c0;
+  }
 }
 
-// Visible keys of a row beside its window range [jlo, jhi]: its document's
-// sinks before it, buffer rows [*slo, *shi] (slo > shi: none). Sinks that touch
-// the window range join it.
-__device__ __forceinline__ void sink_interval(const Geom& g, int doc_start, int* jlo, int* slo, int* shi) {
-  *slo = 1;
-  *shi = 0;
-  if (g.window <= 0 || g.n_sink <= 0) return;
+// The keys a row sees beside its window [jlo, ...]: buffer rows [slo, shi], its
+// document's sinks before the window (slo > shi: none). `inner`: they are seen in
+// the window passes, as the document starts inside the q tile that starts at
+// global position p0 (only with W < kTile does that leave any), not in the sink
+// passes.
+struct RowKeys {
+  int slo = 1, shi = 0;
+  bool inner = false;
+};
+__device__ __forceinline__ RowKeys row_sinks(const Geom& g, int doc_start, int jlo, int p0) {
+  RowKeys k;
   const int d = doc_start - g.kv_offset;
-  if (d >= *jlo) return;  // the window reaches the document's start
-  if (d + g.n_sink >= *jlo) {
-    *jlo = d;
-  } else {
-    *slo = d;
-    *shi = d + g.n_sink - 1 < g.S_kv - 1 ? d + g.n_sink - 1 : g.S_kv - 1;  // a K/V chunk may end among them
-  }
+  if (g.window <= 0 || g.n_sink <= 0 || d >= jlo) return k;
+  k.slo = d;
+  k.shi = (d + g.n_sink < jlo ? d + g.n_sink : jlo) - 1;
+  if (k.shi > g.S_kv - 1) k.shi = g.S_kv - 1;  // a K/V chunk may end among them
+  k.inner = doc_start > p0;
+  return k;
+}
+
+// Keep bits [c0, c0 + 32) of a row's 128, c0 a multiple of 16.
+__device__ __forceinline__ uint32_t keep_bits32(const uint32_t (&km)[4], int c0) {
+  const int w = c0 >> 5;
+  const uint32_t lo = w == 0 ? km[0] : w == 1 ? km[1] : w == 2 ? km[2] : km[3];
+  const uint32_t hi = w == 0 ? km[1] : w == 1 ? km[2] : km[3];
+  return (c0 & 16) ? (lo >> 16) | (hi << 16) : lo;
 }
 
 // Units of a sink table, or -1 when the table is not one for this geometry.
@@ -200,27 +216,22 @@ __device__ __forceinline__ int sink_n_units(const Geom& g, const int32_t* seg) {
 }
 
 // Where key row r of a unit's tile goes: >= 0 a row of the unit's partial slot,
-// -1 straight to dk / dv, -2 nowhere (another unit of the tile writes it).
-__device__ __forceinline__ int unit_part_row(const Geom& g, int slot, int flags, int rbase, int r) {
+// -1 straight to dk / dv, -2 nowhere (the tile's primary unit writes it).
+__device__ __forceinline__ int unit_part_row(const Geom& g, int slot, int primary, int rbase, int r) {
   if (slot < 0) return -1;
   if (r >= rbase && r < rbase + g.sk_rows) return r - rbase;
-  return (flags & kUnitPrimary) ? -1 : -2;
+  return primary ? -1 : -2;
 }
 // A slot row of dk (which = 0) or dv (1) of kv head hk.
 __device__ __forceinline__ float* unit_part(const Geom& g, int slot, int hk, int which, int row) {
   return g.sk_part + (((static_cast<size_t>(slot) * g.Hkv + hk) * 2 + which) * g.sk_rows + row) * g.D;
 }
 
-// The rows [beg, end) (global positions) that attend key `key` (doc [ds, de))
-// in a unit: window pairs s <= p < s + W, or sink-only pairs p >= s + W.
-__device__ __forceinline__ void unit_rows(const Geom& g, int key, int ds, int de, bool sink_unit, int* beg, int* end) {
-  if (sink_unit) {
-    *beg = key + g.window;
-    *end = key - ds < g.n_sink ? de : -0x40000000;
-  } else {
-    *beg = key;
-    *end = g.window > 0 && key + g.window < de ? key + g.window : de;
-  }
+// The end of the rows (global positions, from key on) that attend key `key` of
+// document [ds, de): the document's end for a sink, else the window's.
+__device__ __forceinline__ int sink_row_end(const Geom& g, int key, int ds, int de) {
+  if (g.window <= 0 || key - ds < g.n_sink) return de;
+  return key + g.window < de ? key + g.window : de;
 }
 
 // Number of 128-row K/V tiles some local row can attend by position alone:

@@ -49,7 +49,7 @@ struct Dq512Smem {
   uint32_t tmem_base;
   int abort_flag;
   int b, qt, kt_lo, nk, n_real, skip;
-  int x0, nx;  // K/V tiles of the first document's sinks, walked before the window's
+  int x0, nx, col[2];  // kSink: the sink passes, walked before the window's tiles
 };
 static_assert(sizeof(Dq512Smem) + 1024 <= 232448, "shared memory per CTA");
 
@@ -85,9 +85,9 @@ __global__ void __launch_bounds__(kThreads5, 1)
     s.b = b;
     s.qt = qt;
     if constexpr (kSink) {
-      // nk counts the sink tiles too: tile j is x0 + j below nx, kt_lo + j - nx above
+      // nk counts the sink passes too: pass j is tile x0 + j below nx, kt_lo + j - nx above
       s.x0 = s.nx = 0;
-      if (ok) sink_extra_tiles(g, seg, b, qt, n_real, kt_lo, nk, &s.x0, &s.nx);
+      if (ok) sink_passes(g, seg, b, qt, n_real, &s.x0, &s.nx, s.col);
       nk += s.nx;
       s.kt_lo = kt_lo - s.nx;
     } else {
@@ -247,14 +247,14 @@ __global__ void __launch_bounds__(kThreads5, 1)
     const int i = qt * kTile + r;
     const bool real = i < n_real;
     int jlo = 1, jhi = 0;  // allowed K/V buffer rows [jlo, jhi] of this row
-    int slo = 1, shi = 0;  // kSink: and its document's sinks [slo, shi] before them
+    RowKeys sk;            // kSink: and its document's sinks before them
     float nl2 = 0.f, ndl = 0.f;
     if (real) {
       const int p = g.row_offset + i;
       const int doc_start = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + i];
       jlo = row_lo_window(doc_start, p, g.window) - g.kv_offset;
       jhi = min(p - g.kv_offset, g.S_kv - 1);  // a K/V chunk may end before the row
-      if constexpr (kSink) sink_interval(g, doc_start, &jlo, &slo, &shi);
+      if constexpr (kSink) sk = row_sinks(g, doc_start, jlo, g.row_offset + qt * kTile);
       nl2 = lse[row0 + i] * -1.4426950408889634f;
       ndl = delta[row0 + i] * -g.scale;  // dS is formed pre-scaled: scale * P (dP - delta)
     }
@@ -269,21 +269,19 @@ __global__ void __launch_bounds__(kThreads5, 1)
       tc_fence_after();
       const int c0 = tile_of(j) * kTile;
       // a row sees all of this tile, none of it, or part of it
-      // kSink: a row sees the tile through its window or its sinks; both at
-      // once only where the sinks end in the window's first tile
+      // kSink: a sink pass sees the row's sinks, a window pass its window and
+      // its inner sinks [b_lo, b_hi]
       int wlo = jlo, whi = jhi, b_lo = 1, b_hi = 0;
       if constexpr (kSink) {
-        if (shi >= c0 && slo <= c0 + kTile - 1 && slo <= shi) {
-          if (jhi < c0 || jlo > c0 + kTile - 1) {
-            wlo = slo;
-            whi = shi;
-          } else {
-            b_lo = slo - c0;
-            b_hi = shi - c0;
-          }
+        if (j < nx) {
+          wlo = sk.inner ? 1 : sk.slo;
+          whi = sk.inner ? 0 : sk.shi;
+        } else if (sk.inner && sk.shi >= c0 && sk.slo <= c0 + kTile - 1) {
+          b_lo = sk.slo - c0;
+          b_hi = sk.shi - c0;
         }
       }
-      const bool dead = !real || whi < c0 || wlo > c0 + kTile - 1;
+      const bool dead = !real || (b_lo > b_hi && (whi < c0 || wlo > c0 + kTile - 1));
       const bool full = wlo <= c0 && c0 + kTile - 1 <= whi;
       uint32_t pk[2][32];  // dS of keys [64 hf, 64 hf + 64), bf16 pairs
       dq_form_ds<kDrop, kSink>(tbase + lane_off + kColS, tbase + lane_off + kColDp, g.scale, nl2, ndl, dead, full, wlo - c0,

@@ -50,7 +50,7 @@ struct Fwd256Smem {
   uint32_t tmem_base;
   int abort_flag;
   int b, qt, kt_lo, nk, n_real, skip;
-  int x0, nx;  // K/V tiles of the first document's sinks, walked before the window's
+  int x0, nx, col[2];  // kSink: the sink passes, walked before the window's tiles
 };
 static_assert(sizeof(Fwd256Smem) + 1024 <= 232448, "shared memory per CTA");
 static_assert(2 * 2 * kChunkB256 >= kTile * kD256 * 2, "out staging fits ring slots 0-1");
@@ -87,9 +87,9 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
     s.b = b;
     s.qt = qt;
     if constexpr (kSink) {
-      // nk counts the sink tiles too: tile j is x0 + j below nx, kt_lo + j - nx above
+      // nk counts the sink passes too: pass j is tile x0 + j below nx, kt_lo + j - nx above
       s.x0 = s.nx = 0;
-      if (ok) sink_extra_tiles(g, seg, b, qt, n_real, kt_lo, nk, &s.x0, &s.nx);
+      if (ok) sink_passes(g, seg, b, qt, n_real, &s.x0, &s.nx, s.col);
       nk += s.nx;
       s.kt_lo = kt_lo - s.nx;
     } else {
@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
   const int b = s.b, qt = s.qt, kt_lo = s.kt_lo, nk = s.nk, n_real = s.n_real;
   const int x0 = kSink ? s.x0 : 0, nx = kSink ? s.nx : 0;
   auto tile_of = [&](int j) { return kSink && j < nx ? x0 + j : kt_lo + j; };
+  const int col0 = kSink ? s.col[0] : -1, col1 = kSink ? s.col[1] : -1;
+  auto col_of = [&](int j) { return kSink && j < nx ? (j == 0 ? col0 : col1) : -1; };  // >= 0: a 32-key pass
 
   if (nk == 0) {  // no row of this q tile sees a key: zeros and -inf
     if (tid >= 128) {
@@ -191,6 +193,7 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
     // ----------------------------------------------------------- MMA issuer
     constexpr uint32_t idS = idesc_bf16(128, 128, false, false);   // S = Q K^T: both K-major
     constexpr uint32_t idPV = idesc_bf16(128, 128, false, true);   // O half += P V half: V MN-major
+    constexpr uint32_t idS32 = idesc_bf16(128, 32, false, false);  // a sink pass of 32 keys
     const uint64_t dKm = umma_desc_sw128(0, 16, 1024);
     const uint64_t dMN = umma_desc_sw128(0, kChunkB256, 1024);      // 16 KB between a half's two chunks
     const uint32_t a_q = smem_u32(s.q[0]), a_ring = smem_u32(s.ring[0][0]);
@@ -205,6 +208,8 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
     // S(t) = Q K(t)^T into buffer t & 1: two halves of the head dim, 8 k-steps each
     auto issue_s = [&](int t) {
       const uint32_t d = tbase + kColS256 + (t & 1) * 128;
+      const int col = col_of(t);
+      const uint32_t id = kSink && col >= 0 ? idS32 : idS, row_off = kSink && col >= 0 ? col * 128 : 0;
       for (int hf = 0; hf < 2; ++hf) {
         const int slot = take();
         if (slot < 0) return false;
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             umma_ss(d, desc_at(dKm, a_q + (2 * hf + c) * kChunkB256 + ks * 32),
-                    desc_at(dKm, a_ring + slot * 2 * kChunkB256 + c * kChunkB256 + ks * 32), idS,
+                    desc_at(dKm, a_ring + slot * 2 * kChunkB256 + c * kChunkB256 + row_off + ks * 32), id,
                     (hf | c | ks) ? 1u : 0u);
         umma_commit(&s.empty[slot]);
         ++u;
@@ -226,10 +231,19 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
       for (int hf = 0; hf < 2; ++hf) {
         const int slot = take();
         if (slot < 0) return false;
+        const int col = col_of(t);
+        if (kSink && col >= 0) {
 #pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks)
-          umma_ts(tbase + kColO256 + hf * 128, tbase + kColS256 + (t & 1) * 128 + ks * 8,
-                  desc_at(dMN, a_ring + slot * 2 * kChunkB256 + ks * 2048), idPV, (t > 0 || ks > 0) ? 1u : 0u);
+          for (int ks = 0; ks < 2; ++ks)
+            umma_ts(tbase + kColO256 + hf * 128, tbase + kColS256 + (t & 1) * 128 + ks * 8,
+                    desc_at(dMN, a_ring + slot * 2 * kChunkB256 + col * 128 + ks * 2048), idPV,
+                    (t > 0 || ks > 0) ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            umma_ts(tbase + kColO256 + hf * 128, tbase + kColS256 + (t & 1) * 128 + ks * 8,
+                    desc_at(dMN, a_ring + slot * 2 * kChunkB256 + ks * 2048), idPV, (t > 0 || ks > 0) ? 1u : 0u);
+        }
         umma_commit(&s.empty[slot]);
         ++u;
       }
@@ -260,88 +274,19 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
     const int i = qt * kTile + r;
     const bool real = i < n_real;
     int jlo = 1, jhi = 0;  // allowed K/V buffer rows [jlo, jhi] of this row
-    int slo = 1, shi = 0;  // kSink: and its document's sinks [slo, shi] before them
+    RowKeys sk;            // kSink: and its document's sinks before them
     if (real) {
       const int p = g.row_offset + i;
       const int doc_start = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + i];
       jlo = row_lo_window(doc_start, p, g.window) - g.kv_offset;
       jhi = min(p - g.kv_offset, g.S_kv - 1);  // a K/V chunk may end before the row
-      if constexpr (kSink) sink_interval(g, doc_start, &jlo, &slo, &shi);
+      if constexpr (kSink) sk = row_sinks(g, doc_start, jlo, g.row_offset + qt * kTile);
     }
     const float sl2 = g.scale * 1.4426950408889634f;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int t = 0; t < nk; ++t) {
-      uint32_t km[4];  // dropout: keep bits of this row over the tile's 128 keys
-      if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + tile_of(t) * kTile, km);
-      if (!warp_wait(&s.s_full[t & 1], (t >> 1) & 1, &s.abort_flag, vstatus)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t t_s = tbase + lane_off + kColS256 + (t & 1) * 128;  // this tile's S buffer
-      // S in two halves: the second half's load is in flight while the first
-      // half's max is formed
-      uint32_t xr[128];
-      tmem_ld32(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&xr[0]));
-      tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&xr[32]));
-      tmem_wait_ld();
-      tmem_regs_ready<64>(&xr[0]);
-      tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&xr[64]));
-      tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&xr[96]));
-      const int c0 = tile_of(t) * kTile;
-      // a row either sees the whole tile, none of it, or part of it; only a
-      // warp with a partly seen row needs the per-element mask
-      // (kSink: a row sees the tile through its window or its sinks; both at
-      // once only where the sinks end in the window's first tile)
-      int wlo = jlo, whi = jhi;
-      bool both = false;
-      if constexpr (kSink) {
-        if (shi >= c0 && slo <= c0 + kTile - 1 && slo <= shi) {
-          both = !(jhi < c0 || jlo > c0 + kTile - 1);
-          if (!both) {
-            wlo = slo;
-            whi = shi;
-          }
-        }
-        both = __any_sync(0xffffffffu, both);
-      }
-      const bool dead = whi < c0 || wlo > c0 + kTile - 1;
-      const bool unmasked = __all_sync(0xffffffffu, dead || (wlo <= c0 && c0 + kTile - 1 <= whi));
-      const int a_lo = wlo - c0, e_hi = whi - c0;
-      float x[128];  // raw scores, -inf where masked
-      float mx[8];   // eight independent 16-column maxima (short dependency chains)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (hf == 1) {
-          tmem_wait_ld();
-          tmem_regs_ready<64>(&xr[64]);
-        }
-        if (unmasked) {
-#pragma unroll
-          for (int c = 64 * hf; c < 64 * hf + 64; ++c) x[c] = __uint_as_float(xr[c]);
-        } else {
-#pragma unroll
-          for (int c = 64 * hf; c < 64 * hf + 64; ++c) x[c] = (c >= a_lo && c <= e_hi) ? __uint_as_float(xr[c]) : -INFINITY;
-          if constexpr (kSink) {
-            if (both) {
-              const int b_lo = slo - c0, b_hi = shi - c0;
-#pragma unroll
-              for (int c = 64 * hf; c < 64 * hf + 64; ++c)
-                if (c >= b_lo && c <= b_hi) x[c] = __uint_as_float(xr[c]);
-            }
-          }
-        }
-#pragma unroll
-        for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
-          float a = fmax3(x[16 * k], x[16 * k + 1], x[16 * k + 2]);
-#pragma unroll
-          for (int c = 16 * k + 3; c < 16 * k + 15; c += 2) a = fmax3(a, x[c], x[c + 1]);
-          mx[k] = fmaxf(a, x[16 * k + 15]);
-        }
-      }
-      float tmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-      tmax = dead ? -INFINITY : tmax * sl2;  // the scale is positive: the max of the scaled scores
+    // the running maximum after a tile's; O and the sum are rescaled once it grew by 2^8
+    auto raise_max = [&](float tmax, int step) -> bool {
       const float m_new = fmaxf(m, tmax);
       const bool need = m_new > m + 8.0f;
       if (__any_sync(0xffffffffu, need)) {
@@ -350,10 +295,9 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
           l *= alpha;
           m = m_new;
         }
-        if (t > 0) {  // rescale the running O once the last PV products are done
-          if (!warp_wait(&s.o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &s.abort_flag, vstatus)) {
-            ok = false;
-            break;
+        if (step > 0) {  // rescale the running O once the last PV products are done
+          if (!warp_wait(&s.o_done[(step - 1) & 1], ((step - 1) >> 1) & 1, &s.abort_flag, vstatus)) {
+            return false;
           }
           tc_fence_after();
 #pragma unroll 1
@@ -372,6 +316,121 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
           }
           tmem_wait_st();
         }
+      }
+      return true;
+    };
+    for (int t = 0; t < nk; ++t) {
+      uint32_t km[4];  // dropout: keep bits of this row over the tile's 128 keys
+      if constexpr (kDrop) row_keep_mask(g, b, h, g.row_offset + i, g.kv_offset + tile_of(t) * kTile, km);
+      if (!warp_wait(&s.s_full[t & 1], (t >> 1) & 1, &s.abort_flag, vstatus)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t t_s = tbase + lane_off + kColS256 + (t & 1) * 128;  // this tile's S buffer
+      if (kSink && col_of(t) >= 0) {
+        // 32 keys of a sink tile: S in the first 32 columns, P over them
+        uint32_t xs[32];
+        tmem_ld32(t_s, xs);
+        tmem_wait_ld();
+        tmem_regs_ready<32>(xs);
+        const int c0 = tile_of(t) * kTile + col_of(t);
+        const int a_lo = sk.inner ? 1 : sk.slo - c0, e_hi = sk.inner ? 0 : sk.shi - c0;
+        const bool dead = a_lo > e_hi || e_hi < 0 || a_lo > 31;
+        float x[32], tmax = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          x[c] = (c >= a_lo && c <= e_hi) ? __uint_as_float(xs[c]) : -INFINITY;
+          tmax = fmaxf(tmax, x[c]);
+        }
+        tmax = dead ? -INFINITY : tmax * sl2;
+        if (!raise_max(tmax, t)) {
+          ok = false;
+          break;
+        }
+        const float nmm = dead ? -INFINITY : (m == -INFINITY) ? 0.f : -m;
+        uint32_t kb = 0;
+        if constexpr (kDrop) kb = keep_bits32(km, col_of(t));
+        float rs = 0.f;
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float p0 = dead ? 0.f : fast_exp2(fmaf(x[2 * c], sl2, nmm));
+          const float p1 = dead ? 0.f : fast_exp2(fmaf(x[2 * c + 1], sl2, nmm));
+          rs += p0 + p1;
+          if constexpr (kDrop)
+            pk[c] = pack_bf16x2((kb >> (2 * c) & 1u) ? p0 : 0.f, (kb >> (2 * c + 1) & 1u) ? p1 : 0.f);
+          else
+            pk[c] = pack_bf16x2(p0, p1);
+        }
+        l += rs;
+        tmem_st16(t_s, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&s.p_full[t & 1]);
+        continue;
+      }
+      // S in two halves: the second half's load is in flight while the first
+      // half's max is formed
+      uint32_t xr[128];
+      tmem_ld32(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&xr[0]));
+      tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&xr[32]));
+      tmem_wait_ld();
+      tmem_regs_ready<64>(&xr[0]);
+      tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&xr[64]));
+      tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&xr[96]));
+      const int c0 = tile_of(t) * kTile;
+      // a row either sees the whole tile, none of it, or part of it; only a
+      // warp with a partly seen row needs the per-element mask
+      // (kSink: a sink pass sees the row's sinks, a window pass its window and,
+      // in a tile with inner sinks, these)
+      int wlo = jlo, whi = jhi;
+      bool inner = false;
+      if constexpr (kSink) {
+        if (t < nx) {
+          wlo = sk.inner ? 1 : sk.slo;
+          whi = sk.inner ? 0 : sk.shi;
+        } else {
+          inner = sk.inner && sk.shi >= c0 && sk.slo <= c0 + kTile - 1;
+        }
+      }
+      const bool any_inner = kSink && __any_sync(0xffffffffu, inner);
+      const bool dead = !inner && (whi < c0 || wlo > c0 + kTile - 1);
+      const bool unmasked = __all_sync(0xffffffffu, dead || (wlo <= c0 && c0 + kTile - 1 <= whi));
+      const int a_lo = wlo - c0, e_hi = whi - c0;
+      float x[128];  // raw scores, -inf where masked
+      float mx[8];   // eight independent 16-column maxima (short dependency chains)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if (hf == 1) {
+          tmem_wait_ld();
+          tmem_regs_ready<64>(&xr[64]);
+        }
+        if (unmasked) {
+#pragma unroll
+          for (int c = 64 * hf; c < 64 * hf + 64; ++c) x[c] = __uint_as_float(xr[c]);
+        } else if (kSink && any_inner) {
+          const int b_lo = inner ? sk.slo - c0 : 1, b_hi = inner ? sk.shi - c0 : 0;
+#pragma unroll
+          for (int c = 64 * hf; c < 64 * hf + 64; ++c)
+            x[c] = ((c >= a_lo && c <= e_hi) || (c >= b_lo && c <= b_hi)) ? __uint_as_float(xr[c]) : -INFINITY;
+        } else {
+#pragma unroll
+          for (int c = 64 * hf; c < 64 * hf + 64; ++c) x[c] = (c >= a_lo && c <= e_hi) ? __uint_as_float(xr[c]) : -INFINITY;
+        }
+#pragma unroll
+        for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
+          float a = fmax3(x[16 * k], x[16 * k + 1], x[16 * k + 2]);
+#pragma unroll
+          for (int c = 16 * k + 3; c < 16 * k + 15; c += 2) a = fmax3(a, x[c], x[c + 1]);
+          mx[k] = fmaxf(a, x[16 * k + 15]);
+        }
+      }
+      float tmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+      tmax = dead ? -INFINITY : tmax * sl2;  // the scale is positive: the max of the scaled scores
+      if (!raise_max(tmax, t)) {
+        ok = false;
+        break;
       }
       // exponent offset; -inf on a row that sees nothing of this tile, so P = 0
       const float nmm = dead ? -INFINITY : (m == -INFINITY) ? 0.f : -m;

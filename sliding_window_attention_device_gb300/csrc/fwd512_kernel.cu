@@ -50,7 +50,7 @@ struct Fwd512Smem {
   uint32_t tmem_base;
   int abort_flag;
   int b, qt, kt_lo, nk, n_real, skip;
-  int x0, nx;  // K/V tiles of the first document's sinks, walked before the window's
+  int x0, nx, col[2];  // kSink: the sink passes, walked before the window's tiles
 };
 
 // kMerge: merge this K/V chunk's result into the running (out, lse) instead
@@ -86,9 +86,9 @@ __global__ void __launch_bounds__(kThreads512, 1)
     s.b = b;
     s.qt = qt;
     if constexpr (kSink) {
-      // nk counts the sink tiles too: tile j is x0 + j below nx, kt_lo + j - nx above
+      // nk counts the sink passes too: pass j is tile x0 + j below nx, kt_lo + j - nx above
       s.x0 = s.nx = 0;
-      if (ok) sink_extra_tiles(g, seg, b, qt, n_real, kt_lo, nk, &s.x0, &s.nx);
+      if (ok) sink_passes(g, seg, b, qt, n_real, &s.x0, &s.nx, s.col);
       nk += s.nx;
       s.kt_lo = kt_lo - s.nx;
     } else {
@@ -119,6 +119,8 @@ __global__ void __launch_bounds__(kThreads512, 1)
   const int b = s.b, qt = s.qt, kt_lo = s.kt_lo, nk = s.nk, n_real = s.n_real;
   const int x0 = kSink ? s.x0 : 0, nx = kSink ? s.nx : 0;
   auto tile_of = [&](int j) { return kSink && j < nx ? x0 + j : kt_lo + j; };
+  const int col0 = kSink ? s.col[0] : -1, col1 = kSink ? s.col[1] : -1;
+  auto col_of = [&](int j) { return kSink && j < nx ? (j == 0 ? col0 : col1) : -1; };  // >= 0: a 32-key pass
 
   if (nk == 0) {  // no row of this q tile sees a key: zeros and -inf
     if (tid >= 128) {
@@ -196,6 +198,7 @@ __global__ void __launch_bounds__(kThreads512, 1)
     // ----------------------------------------------------------- MMA issuer
     constexpr uint32_t idS = idesc_bf16(128, 128, false, false);   // S = Q K^T: both K-major
     constexpr uint32_t idPV = idesc_bf16(128, 256, false, true);   // O half += P V half: V MN-major
+    constexpr uint32_t idS32 = idesc_bf16(128, 32, false, false);  // a sink pass of 32 keys
     const uint64_t dK_major = umma_desc_sw128(0, 16, 1024);
     const uint64_t dMN = umma_desc_sw128(0, kChunkB, 1024);          // 16 KB between 64-column chunks
     const uint32_t a_q = smem_u32(s.q[0]), a_k = smem_u32(s.k[0]), a_v = smem_u32(s.v[0]);
@@ -205,14 +208,16 @@ __global__ void __launch_bounds__(kThreads512, 1)
     // S(u) = Q K^T over the 8 head-dim chunks into buffer u & 1
     auto issue_s = [&](int u) {
       const uint32_t d = tbase + kColS + (u & 1) * 128;
+      const int col = col_of(u % nk);
+      const uint32_t id = kSink && col >= 0 ? idS32 : idS, row_off = kSink && col >= 0 ? col * 128 : 0;
       for (int c = 0; c < kQChunks; ++c, ++kc) {
         const int slot = kc % kKSlots;
         if (!wait(&s.k_full[slot], (kc / kKSlots) & 1)) return false;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma_ss(d, desc_at(dK_major, a_q + c * kChunkB + ks * 32), desc_at(dK_major, a_k + slot * kChunkB + ks * 32),
-                  idS, (c > 0 || ks > 0) ? 1u : 0u);
+          umma_ss(d, desc_at(dK_major, a_q + c * kChunkB + ks * 32),
+                  desc_at(dK_major, a_k + slot * kChunkB + row_off + ks * 32), id, (c > 0 || ks > 0) ? 1u : 0u);
         umma_commit(&s.k_empty[slot]);
       }
       umma_commit(&s.s_full[u & 1]);
@@ -228,10 +233,18 @@ __global__ void __launch_bounds__(kThreads512, 1)
         break;
       }
       tc_fence_after();
+      const int col = col_of(j);
+      if (kSink && col >= 0) {
 #pragma unroll
-      for (int ks = 0; ks < kTile / 16; ++ks)
-        umma_ts(tbase + kColO, tbase + kColS + (t & 1) * 128 + ks * 8, desc_at(dMN, a_v + ks * 2048), idPV,
-                (j > 0 || ks > 0) ? 1u : 0u);
+        for (int ks = 0; ks < 2; ++ks)
+          umma_ts(tbase + kColO, tbase + kColS + (t & 1) * 128 + ks * 8, desc_at(dMN, a_v + col * 128 + ks * 2048),
+                  idPV, (j > 0 || ks > 0) ? 1u : 0u);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < kTile / 16; ++ks)
+          umma_ts(tbase + kColO, tbase + kColS + (t & 1) * 128 + ks * 8, desc_at(dMN, a_v + ks * 2048), idPV,
+                  (j > 0 || ks > 0) ? 1u : 0u);
+      }
       umma_commit(&s.v_empty);
       umma_commit(&s.o_done[t & 1]);
       // S two steps on goes into the buffer this PV product reads (issued after it)
@@ -254,13 +267,13 @@ __global__ void __launch_bounds__(kThreads512, 1)
     const int i = qt * kTile + r;
     const bool real = i < n_real;
     int jlo = 1, jhi = 0;  // allowed K/V buffer rows [jlo, jhi] of this row
-    int slo = 1, shi = 0;  // kSink: and its document's sinks [slo, shi] before them
+    RowKeys sk;            // kSink: and its document's sinks before them
     if (real) {
       const int p = g.row_offset + i;
       const int doc_start = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + i];
       jlo = row_lo_window(doc_start, p, g.window) - g.kv_offset;
       jhi = min(p - g.kv_offset, g.S_kv - 1);
-      if constexpr (kSink) sink_interval(g, doc_start, &jlo, &slo, &shi);
+      if constexpr (kSink) sk = row_sinks(g, doc_start, jlo, g.row_offset + qt * kTile);
     }
     const size_t row = (static_cast<size_t>(b) * g.Hq + h) * g.L + i;
     const float sl2 = g.scale * 1.4426950408889634f;
@@ -271,6 +284,40 @@ __global__ void __launch_bounds__(kThreads512, 1)
     bool store = false;
     float w_old = 0.f, w_new = 1.f;
     bool ok = true, empty = true;             // empty: the row sees no key at all
+    // the running maximum after a tile's; O and the sum are rescaled once it grew by 2^8
+    auto raise_max = [&](float tmax, int j, int t) -> bool {
+      const float m_new = fmaxf(m, tmax);
+      const bool need = m_new > m + 8.0f;
+      if (__any_sync(0xffffffffu, need)) {
+        const float alpha = need ? fast_exp2(m - m_new) : 1.0f;
+        if (need) {
+          l *= alpha;
+          m = m_new;
+        }
+        if (j > 0) {  // rescale the running O once its last product is done
+          if (!warp_wait(&s.o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &s.abort_flag, vstatus)) {
+            return false;
+          }
+          tc_fence_after();
+          const float2 av = make_float2(alpha, alpha);
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), av);
+              o[e] = __float_as_uint(v.x);
+              o[e + 1] = __float_as_uint(v.y);
+            }
+            tmem_st32(t_o + c, o);
+          }
+          tmem_wait_st();
+        }
+      }
+      return true;
+    };
     int t = 0;
     for (int p = 0; p < 2 && ok; ++p) {
       for (int j = 0; j < nk; ++j, ++t) {
@@ -282,6 +329,50 @@ __global__ void __launch_bounds__(kThreads512, 1)
         }
         tc_fence_after();
         const uint32_t t_s = tbase + lane_off + kColS + (t & 1) * 128;  // this step's S buffer
+        if (kSink && col_of(j) >= 0) {
+          // 32 keys of a sink tile: S in the first 32 columns, P over them
+          uint32_t xs[32];
+          tmem_ld32(t_s, xs);
+          tmem_wait_ld();
+          tmem_regs_ready<32>(xs);
+          const int c0 = tile_of(j) * kTile + col_of(j);
+          const int a_lo = sk.inner ? 1 : sk.slo - c0, e_hi = sk.inner ? 0 : sk.shi - c0;
+          const bool dead = a_lo > e_hi || e_hi < 0 || a_lo > 31;
+          float nmm = nl2;
+          if (p == 0) {
+            float tmax = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c >= a_lo && c <= e_hi) tmax = fmaxf(tmax, __uint_as_float(xs[c]));
+            if (!raise_max(dead ? -INFINITY : tmax * sl2, j, t)) {
+              ok = false;
+              break;
+            }
+            nmm = (m == -INFINITY) ? 0.f : -m;
+          }
+          const bool zero = dead || (p == 1 && empty);
+          uint32_t kb = 0;
+          if constexpr (kDrop) kb = keep_bits32(km, col_of(j));
+          float rs = 0.f;
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const bool in0 = !zero && 2 * c >= a_lo && 2 * c <= e_hi, in1 = !zero && 2 * c + 1 >= a_lo && 2 * c + 1 <= e_hi;
+            const float p0 = in0 ? fast_exp2(fmaf(__uint_as_float(xs[2 * c]), sl2, nmm)) : 0.f;
+            const float p1 = in1 ? fast_exp2(fmaf(__uint_as_float(xs[2 * c + 1]), sl2, nmm)) : 0.f;
+            rs += p0 + p1;
+            if constexpr (kDrop)
+              pk[c] = pack_bf16x2((kb >> (2 * c) & 1u) ? p0 : 0.f, (kb >> (2 * c + 1) & 1u) ? p1 : 0.f);
+            else
+              pk[c] = pack_bf16x2(p0, p1);
+          }
+          if (p == 0) l += rs;
+          tmem_st16(t_s, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&s.p_full[t & 1]);
+          continue;
+        }
         uint32_t xr[128];
         tmem_ld32(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&xr[0]));
         tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&xr[32]));
@@ -290,63 +381,43 @@ __global__ void __launch_bounds__(kThreads512, 1)
         tmem_wait_ld();
         tmem_regs_ready<128>(xr);
         const int c0 = tile_of(j) * kTile;
-        // kSink: a row sees the tile through its window or its sinks; both at
-        // once only where the sinks end in the window's first tile
-        int wlo = jlo, whi = jhi, b_lo = 1, b_hi = 0;
+        // kSink: a sink pass sees the row's sinks, a window pass its window and,
+        // in a tile with inner sinks, these (masked here, once for both uses)
+        int wlo = jlo, whi = jhi;
+        bool inner = false;
         if constexpr (kSink) {
-          if (shi >= c0 && slo <= c0 + kTile - 1 && slo <= shi) {
-            if (jhi < c0 || jlo > c0 + kTile - 1) {
-              wlo = slo;
-              whi = shi;
-            } else {
-              b_lo = slo - c0;
-              b_hi = shi - c0;
+          if (j < nx) {
+            wlo = sk.inner ? 1 : sk.slo;
+            whi = sk.inner ? 0 : sk.shi;
+          } else {
+            inner = sk.inner && sk.shi >= c0 && sk.slo <= c0 + kTile - 1;
+          }
+          if (__any_sync(0xffffffffu, inner)) {
+            const int a_lo = wlo - c0, e_hi = whi - c0, b_lo = inner ? sk.slo - c0 : 1, b_hi = inner ? sk.shi - c0 : 0;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (!((c >= a_lo && c <= e_hi) || (c >= b_lo && c <= b_hi))) xr[c] = 0xff800000u;  // -inf
+            if (inner) {
+              wlo = c0;
+              whi = c0 + kTile - 1;
             }
           }
         }
         const bool dead = whi < c0 || wlo > c0 + kTile - 1;
         const bool full = wlo <= c0 && c0 + kTile - 1 <= whi;
         const int a_lo = wlo - c0, e_hi = whi - c0;
-        auto sees = [&](int c) { return (c >= a_lo && c <= e_hi) || (kSink && c >= b_lo && c <= b_hi); };
         float nmm;  // exponent offset
         if (p == 0) {
           float tmax = -INFINITY;
           if (!dead) {
 #pragma unroll
             for (int c = 0; c < 128; ++c)
-              if (full || sees(c)) tmax = fmaxf(tmax, __uint_as_float(xr[c]));
+              if (full || (c >= a_lo && c <= e_hi)) tmax = fmaxf(tmax, __uint_as_float(xr[c]));
             tmax *= sl2;
           }
-          const float m_new = fmaxf(m, tmax);
-          const bool need = m_new > m + 8.0f;
-          if (__any_sync(0xffffffffu, need)) {
-            const float alpha = need ? fast_exp2(m - m_new) : 1.0f;
-            if (need) {
-              l *= alpha;
-              m = m_new;
-            }
-            if (j > 0) {  // rescale the running O once its last product is done
-              if (!warp_wait(&s.o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &s.abort_flag, vstatus)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const float2 av = make_float2(alpha, alpha);
-#pragma unroll 1
-              for (int c = 0; c < 256; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(t_o + c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), av);
-                  o[e] = __float_as_uint(v.x);
-                  o[e + 1] = __float_as_uint(v.y);
-                }
-                tmem_st32(t_o + c, o);
-              }
-              tmem_wait_st();
-            }
+          if (!raise_max(tmax, j, t)) {
+            ok = false;
+            break;
           }
           nmm = (m == -INFINITY) ? 0.f : -m;
         } else {
@@ -364,8 +435,8 @@ __global__ void __launch_bounds__(kThreads512, 1)
             p0 = 0.f;
             p1 = 0.f;
           } else if (!full) {
-            p0 = sees(2 * c) ? p0 : 0.f;
-            p1 = sees(2 * c + 1) ? p1 : 0.f;
+            p0 = (2 * c >= a_lo && 2 * c <= e_hi) ? p0 : 0.f;
+            p1 = (2 * c + 1 >= a_lo && 2 * c + 1 <= e_hi) ? p1 : 0.f;
           }
           rs2 = __fadd2_rn(rs2, make_float2(p0, p1));
           if constexpr (kDrop) {

@@ -71,7 +71,7 @@ __device__ int block_exclusive_scan(int v, int* s_red, int* total) {
 }  // namespace
 
 // The sink-only rows of K/V tile kt of batch row b (local rows [sb, se), none
-// if sb >= se) and the tile row rbase from which its sinks with such rows start.
+// if sb >= se) and the tile row rbase from which its last document's keys start.
 // A superset: the kernels mask pair by pair.
 __device__ void sink_tile_rows(const Geom& g, const int32_t* seg, int b, int kt, int* sb, int* se, int* rbase) {
   *sb = *se = *rbase = 0;
@@ -102,15 +102,12 @@ __device__ void sink_tile_rows(const Geom& g, const int32_t* seg, int b, int kt,
     end = de - ro;
   }
   *rbase = first - s_lo;
-  if (g.window < kTile) {  // earlier documents of the tile may have such rows inside it
-    if (ds > k_lo) {
-      const int beg2 = max(0, k_lo + g.window - ro), end2 = ds - ro;
-      if (beg2 < end2) {
-        beg = min(beg, beg2);
-        end = max(end, end2);
-      }
+  if (g.window < kTile && ds > k_lo) {  // earlier documents of the tile may have such rows inside it
+    const int beg2 = max(0, k_lo + g.window - ro), end2 = ds - ro;
+    if (beg2 < end2) {
+      beg = min(beg, beg2);
+      end = max(end, end2);
     }
-    *rbase = 0;
   }
   if (beg < end) {
     *sb = beg;
@@ -291,12 +288,115 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
   }
 }
 
-// A single CTA classifies every tile of every batch row and builds the two
-// longest-first work lists. Dynamic shared memory: (nbins) ints of histogram.
-__global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restrict__ seg, int nbins) {
+// The backward's units of a sink table (one CTA; see common.cuh), longest
+// first; partial slots numbered in tile order, so the order in which the last
+// kernel adds them does not depend on the run. s_hist: nbins ints of histogram.
+__device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int nbins, int32_t* status, int* s_hist,
+                                 int* s_red) {
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  int32_t* hdr = seg + g.sk_off;
+  int32_t* units = hdr + kSinkHdrWords;
+  int32_t* sums = units + static_cast<size_t>(g.sk_units) * kSinkUnitWords;
+  const int n_items = g.B * g.nkt, span = g.sk_split * kTile;
+  auto bin_of = [&](int beg, int end) { return nbins - 1 - min((end - 1) / kBwdQ - beg / kBwdQ + 1, nbins - 1); };
+  // units of a tile: rows [beg, end0), then pieces of `span` up to end; returns their number
+  auto ranges = [&](int item, int* beg, int* end0, int* end, int* rbase) -> int {
+    const int b = item / g.nkt, kt = item % g.nkt;
+    const int n_real = seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL];
+    int wb, we, sb, se;
+    window_tile_rows(g, seg + g.off[BD_SEG_OFF_ROW_LO] + b * g.L, n_real, kt, &wb, &we);
+    sink_tile_rows(g, seg, b, kt, &sb, &se, rbase);
+    if (wb >= we) {
+      wb = sb;
+      we = sb;
+    } else if (sb < se) {
+      wb = min(wb, sb);
+    }
+    *beg = wb;
+    *end = max(we, se);
+    if (*beg >= *end) return 0;
+    *end0 = min(*end, max((wb / kTile) * kTile + span, cdiv(we, kTile) * kTile));
+    return 1 + cdiv(*end - *end0, span);
+  };
+  for (int x = tid; x < nbins; x += nthr) s_hist[x] = 0;
+  __syncthreads();
+  int n_units = 0;
+  for (int item = tid; item < n_items; item += nthr) {
+    int beg, end0, end, rbase;
+    const int n = ranges(item, &beg, &end0, &end, &rbase);
+    for (int x = 0; x < n; ++x)
+      atomicAdd(&s_hist[x == 0 ? bin_of(beg, end0) : bin_of(end0 + (x - 1) * span, min(end, end0 + x * span))], 1);
+    n_units += n;
+  }
+  n_units = block_reduce(n_units, AddOp(), s_red);
+  int carry = 0;  // exclusive scan of the histogram, in chunks of blockDim
+  for (int c0 = 0; c0 < nbins; c0 += nthr) {
+    const int x = c0 + tid;
+    const int v = x < nbins ? s_hist[x] : 0;
+    int tot;
+    const int ex = block_exclusive_scan(v, s_red, &tot);
+    __syncthreads();
+    if (x < nbins) s_hist[x] = carry + ex;
+    carry += tot;
+    __syncthreads();
+  }
+  int n_sums = 0, n_slots = 0;
+  bool over = n_units > g.sk_units;
+  for (int c0 = 0; c0 < n_items; c0 += nthr) {
+    const int item = c0 + tid;
+    int beg = 0, end0 = 0, end = 0, rbase = 0, n = 0;
+    if (item < n_items) n = ranges(item, &beg, &end0, &end, &rbase);
+    const int multi = n > 1;
+    int tot_sums, tot_slots;
+    const int sum = n_sums + block_exclusive_scan(multi, s_red, &tot_sums);
+    const int slot0 = n_slots + block_exclusive_scan(multi ? n : 0, s_red, &tot_slots);
+    if (multi && (sum >= g.sk_sums || slot0 + n > g.sk_slots)) over = true;
+    if (multi && sum < g.sk_sums) {
+      int32_t* e = sums + static_cast<size_t>(sum) * kSinkSumWords;
+      e[0] = item;
+      e[1] = slot0;
+      e[2] = n;
+      e[3] = rbase;
+    }
+    for (int x = 0; x < n; ++x) {
+      const int ub = x == 0 ? beg : end0 + (x - 1) * span, ue = x == 0 ? end0 : min(end, end0 + x * span);
+      const int pos = atomicAdd(&s_hist[bin_of(ub, ue)], 1);
+      if (pos >= g.sk_units) continue;
+      int32_t* u = units + static_cast<size_t>(pos) * kSinkUnitWords;
+      u[0] = item;
+      u[1] = ub;
+      u[2] = ue;
+      u[3] = x == 0;
+      u[4] = multi ? slot0 + x : -1;
+      u[5] = rbase;
+      u[6] = u[7] = 0;
+    }
+    n_sums += tot_sums;
+    n_slots += tot_slots;
+  }
+  over = block_reduce(over ? 1 : 0, OrOp(), s_red) != 0;
+  if (tid == 0) {
+    // an overflow would be an error of the capacities: nothing is run on the table
+    hdr[0] = over ? -1 : n_units;
+    hdr[1] = over ? -1 : n_sums;
+    hdr[2] = n_slots;
+    for (int x = 3; x < kSinkHdrWords; ++x) hdr[x] = 0;
+    if (over) atomicOr(status, BD_STATUS_BOUNDS);
+  }
+}
+
+// CTA 0 classifies every tile of every batch row and builds the two
+// longest-first work lists; CTA 1, launched for sink tables, builds the
+// backward's units, which need nothing of CTA 0's. Dynamic shared memory: (nbins) ints of histogram.
+__global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restrict__ seg, int nbins,
+                                                        int32_t* status) {
   pdl_begin();
   extern __shared__ int s_hist[];
   __shared__ int s_red[32];
+  if (blockIdx.x == 1) {
+    build_sink_units(g, seg, nbins, status, s_hist, s_red);
+    return;
+  }
   const int tid = threadIdx.x, nthr = blockDim.x;
   const int ro = g.row_offset, L = g.L, W = g.window;
   int n_full = 0, n_part = 0, n_kv_att = 0;
@@ -391,9 +491,9 @@ __global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restr
         key = qk[1] >= qk[0] ? qk[1] - qk[0] + 1 : 0;
         if (g.n_sink > 0) {
           const int b = item / g.nqt;
-          int x0, nx;
-          sink_extra_tiles(g, seg, b, item % g.nqt, seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL],
-                           qk[0], key, &x0, &nx);
+          int x0, nx, col[2];
+          sink_passes(g, seg, b, item % g.nqt, seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL], &x0,
+                      &nx, col);
           key += nx;
         }
       } else {
@@ -424,114 +524,6 @@ __global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restr
   }
 }
 
-// The backward's units of a sink table (one CTA): every K/V tile's window rows
-// as one unit and its sink-only rows in units of sk_split q tiles, listed
-// longest first; partial slots numbered in tile order, so the order in which
-// the last kernel adds them does not depend on the run. Dynamic shared memory:
-// nbins ints of histogram.
-__global__ void __launch_bounds__(1024) sink_units_kernel(Geom g, int32_t* __restrict__ seg, int nbins,
-                                                          int32_t* status) {
-  pdl_begin();
-  extern __shared__ int s_hist[];
-  __shared__ int s_red[32];
-  const int tid = threadIdx.x, nthr = blockDim.x;
-  int32_t* hdr = seg + g.sk_off;
-  int32_t* units = hdr + kSinkHdrWords;
-  int32_t* sums = units + static_cast<size_t>(g.sk_units) * kSinkUnitWords;
-  const int n_items = g.B * g.nkt, span = g.sk_split * kTile;
-  auto bin_of = [&](int beg, int end) { return nbins - 1 - min((end - 1) / kBwdQ - beg / kBwdQ + 1, nbins - 1); };
-  // unit x of a tile with window rows [wb, we) and sink-only rows [sb, se)
-  auto unit_range = [&](int x, int wb, int we, int sb, int se, int* beg, int* end, int* sink) {
-    const int has_w = wb < we;
-    if (has_w && x == 0) {
-      *beg = wb;
-      *end = we;
-      *sink = 0;
-      return;
-    }
-    const int first = (sb / kTile) * kTile, y = x - has_w;
-    *beg = max(sb, first + y * span);
-    *end = min(se, first + (y + 1) * span);
-    *sink = 1;
-  };
-  auto ranges = [&](int item, int* wb, int* we, int* sb, int* se, int* rbase) -> int {
-    const int b = item / g.nkt, kt = item % g.nkt;
-    const int n_real = seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL];
-    window_tile_rows(g, seg + g.off[BD_SEG_OFF_ROW_LO] + b * g.L, n_real, kt, wb, we);
-    sink_tile_rows(g, seg, b, kt, sb, se, rbase);
-    const int n_s = *sb < *se ? cdiv(*se - (*sb / kTile) * kTile, span) : 0;
-    return (*wb < *we ? 1 : 0) + n_s;
-  };
-  for (int x = tid; x < nbins; x += nthr) s_hist[x] = 0;
-  __syncthreads();
-  int n_units = 0;
-  for (int item = tid; item < n_items; item += nthr) {
-    int wb, we, sb, se, rbase, beg, end, sink;
-    const int n = ranges(item, &wb, &we, &sb, &se, &rbase);
-    for (int x = 0; x < n; ++x) {
-      unit_range(x, wb, we, sb, se, &beg, &end, &sink);
-      atomicAdd(&s_hist[bin_of(beg, end)], 1);
-    }
-    n_units += n;
-  }
-  n_units = block_reduce(n_units, AddOp(), s_red);
-  int carry = 0;  // exclusive scan of the histogram, in chunks of blockDim
-  for (int c0 = 0; c0 < nbins; c0 += nthr) {
-    const int x = c0 + tid;
-    const int v = x < nbins ? s_hist[x] : 0;
-    int tot;
-    const int ex = block_exclusive_scan(v, s_red, &tot);
-    __syncthreads();
-    if (x < nbins) s_hist[x] = carry + ex;
-    carry += tot;
-    __syncthreads();
-  }
-  int n_sums = 0, n_slots = 0;
-  bool over = n_units > g.sk_units;
-  for (int c0 = 0; c0 < n_items; c0 += nthr) {
-    const int item = c0 + tid;
-    int wb = 0, we = 0, sb = 0, se = 0, rbase = 0, n = 0;
-    if (item < n_items) n = ranges(item, &wb, &we, &sb, &se, &rbase);
-    const int multi = n > 1;
-    int tot_sums, tot_slots;
-    const int sum = n_sums + block_exclusive_scan(multi, s_red, &tot_sums);
-    const int slot0 = n_slots + block_exclusive_scan(multi ? n : 0, s_red, &tot_slots);
-    if (multi && (sum >= g.sk_sums || slot0 + n > g.sk_slots)) over = true;
-    if (multi && sum < g.sk_sums) {
-      int32_t* e = sums + static_cast<size_t>(sum) * kSinkSumWords;
-      e[0] = item;
-      e[1] = slot0;
-      e[2] = n;
-      e[3] = rbase;
-    }
-    for (int x = 0; x < n; ++x) {
-      int beg, end, sink;
-      unit_range(x, wb, we, sb, se, &beg, &end, &sink);
-      const int pos = atomicAdd(&s_hist[bin_of(beg, end)], 1);
-      if (pos >= g.sk_units) continue;
-      int32_t* u = units + static_cast<size_t>(pos) * kSinkUnitWords;
-      u[0] = item;
-      u[1] = beg;
-      u[2] = end;
-      u[3] = (sink ? kUnitSink : 0) | (x == 0 ? kUnitPrimary : 0);
-      u[4] = multi ? slot0 + x : -1;
-      u[5] = rbase;
-      u[6] = u[7] = 0;
-    }
-    n_sums += tot_sums;
-    n_slots += tot_slots;
-  }
-  over = block_reduce(over ? 1 : 0, OrOp(), s_red) != 0;
-  if (tid == 0) {
-    // an overflow would be an error of the capacities: nothing is run on the table
-    hdr[0] = over ? -1 : n_units;
-    hdr[1] = over ? -1 : n_sums;
-    hdr[2] = n_slots;
-    for (int x = 3; x < kSinkHdrWords; ++x) hdr[x] = 0;
-    if (over) atomicOr(status, BD_STATUS_BOUNDS);
-  }
-}
-
 cudaError_t launch_seg_build(const int32_t* doc, const Geom& g, int32_t* seg, int32_t* status, cudaStream_t st,
                              int kv_chunk) {
   if (const cudaError_t le = launch_pdl(seg_build_kernel, dim3(g.B), dim3(1024), 0, st, doc, g, seg, status, kv_chunk);
@@ -541,12 +533,8 @@ cudaError_t launch_seg_build(const int32_t* doc, const Geom& g, int32_t* seg, in
   // histogram bins of the work-list sort (48 KB of shared memory at most)
   int nbins = (g.nkt > cdiv(g.L, kBwdQ) ? g.nkt : cdiv(g.L, kBwdQ)) + 1;
   if (nbins > 12288) nbins = 12288;
-  if (const cudaError_t le = launch_pdl(classify_kernel, dim3(1), dim3(1024), static_cast<size_t>(nbins) * 4, st, g,
-      seg, nbins); le != cudaSuccess) return le;
-  if (g.sink_tab) {
-    if (const cudaError_t le = launch_pdl(sink_units_kernel, dim3(1), dim3(1024), static_cast<size_t>(nbins) * 4, st, g,
-        seg, nbins, status); le != cudaSuccess) return le;
-  }
+  if (const cudaError_t le = launch_pdl(classify_kernel, dim3(g.sink_tab ? 2 : 1), dim3(1024),
+      static_cast<size_t>(nbins) * 4, st, g, seg, nbins, status); le != cudaSuccess) return le;
   return cudaGetLastError();
 }
 
