@@ -8,7 +8,6 @@ library, or without a GPU, these functions raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -102,6 +101,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """Load libbdattn.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -468,21 +469,31 @@ def read_seg(seg: torch.Tensor, g: Geom) -> dict:
 SINK_MAX = 128  # BD_SINK_MAX
 
 
-def _on(dev, stream):
-    """Context with `dev` current and new tensors owned by the stream the call
-    runs on, and that stream. The caller's other tensors have to be ready on it."""
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise ValueError(f"the stream is on {s.device}, the tensors are on {dev}")
-    if stream is None and dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), ctypes.c_void_p(s.cuda_stream)
-    return torch.cuda.stream(s), ctypes.c_void_p(s.cuda_stream)
+def _want(t, name: str, dtype, shape, dev):
+    """_need, with one test when nothing is wrong."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_cuda and t.is_contiguous()):
+        _need(t, name, dtype, shape, dev)
 
 
 def _cuda_device(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.device
+
+
+def _elsewhere(dev, stream):
+    """The context in which a call on `stream` (None: the current one of `dev`) runs -- its device and stream
+    current, so that what the call allocates belongs to that stream -- or None when it is that already."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+        return torch.cuda.stream(stream)
+    return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _current(dev) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def sink_seg_bytes(g: Geom, n_sink: int) -> int:
@@ -505,18 +516,19 @@ def bd_attn_sink_seg_build(doc_ids: torch.Tensor, g: Geom, n_sink: int, kv_chunk
     visible past the window; `kv_chunk`: of one chunk of the K/V range. Returns
     (seg, status); `seg` serves every bd_attn_sink_* call of this geometry and n_sink."""
     dev = _cuda_device(doc_ids, "doc_ids")
-    _need(doc_ids, "doc_ids", torch.int32, (g.B, g.S_full), None)
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return bd_attn_sink_seg_build(doc_ids, g, n_sink, kv_chunk, seg, status)
     n = sink_seg_bytes(g, n_sink) // 4
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if seg is None:
-            seg = torch.empty(n, dtype=torch.int32, device=dev)
-        if status is None:
-            status = new_status(dev)
-        _need(seg, "seg", torch.int32, (n,), dev)
-        _need(status, "status", torch.int32, (1,), dev)
-        _check(load().bd_attn_sink_seg_build(_ptr(doc_ids), ctypes.byref(g), int(n_sink), int(bool(kv_chunk)),
-                                             _ptr(seg), _ptr(status), st), "bd_attn_sink_seg_build")
+    if seg is None:
+        seg = torch.empty(n, dtype=torch.int32, device=dev)
+    if status is None:
+        status = new_status(dev)
+    _want(doc_ids, "doc_ids", torch.int32, (g.B, g.S_full), dev)
+    _want(seg, "seg", torch.int32, (n,), dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    _check(load().bd_attn_sink_seg_build(doc_ids.data_ptr(), ctypes.byref(g), int(n_sink), int(bool(kv_chunk)),
+                                         seg.data_ptr(), status.data_ptr(), _current(dev)), "bd_attn_sink_seg_build")
     return seg, status
 
 
@@ -524,21 +536,23 @@ def bd_attn_sink_fwd(q, k, v, seg, g: Geom, n_sink: int, status, out=None, lse=N
                      _fn="bd_attn_sink_fwd"):
     """bd_attn_fwd with the documents' first n_sink tokens visible past the window."""
     dev = _cuda_device(q, "q")
-    _need(q, "q", torch.bfloat16, (g.B, g.Hq, g.L, g.D), dev)
-    _need(k, "k", torch.bfloat16, kv_shape(g), dev)
-    _need(v, "v", torch.bfloat16, kv_shape(g), dev)
-    _need(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
-    _need(status, "status", torch.int32, (1,), dev)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty(g.B, g.Hq, g.L, g.D, dtype=torch.bfloat16, device=dev)
-        if lse is None:
-            lse = torch.empty(g.B, g.Hq, g.L, dtype=torch.float32, device=dev)
-        _need(out, "out", torch.bfloat16, (g.B, g.Hq, g.L, g.D), dev)
-        _need(lse, "lse", torch.float32, (g.B, g.Hq, g.L), dev)
-        _check(getattr(load(), _fn)(_ptr(q), _ptr(k), _ptr(v), _ptr(seg), ctypes.byref(g), int(n_sink), _ptr(out),
-                                    _ptr(lse), _ptr(status), st), _fn)
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return bd_attn_sink_fwd(q, k, v, seg, g, n_sink, status, out, lse, None, _fn)
+    rows, kv = (g.B, g.Hq, g.L, g.D), kv_shape(g)
+    _want(q, "q", torch.bfloat16, rows, dev)
+    _want(k, "k", torch.bfloat16, kv, dev)
+    _want(v, "v", torch.bfloat16, kv, dev)
+    _want(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(rows[:3], dtype=torch.float32, device=dev)
+    _want(out, "out", torch.bfloat16, rows, dev)
+    _want(lse, "lse", torch.float32, rows[:3], dev)
+    _check(getattr(load(), _fn)(q.data_ptr(), k.data_ptr(), v.data_ptr(), seg.data_ptr(), ctypes.byref(g),
+                                int(n_sink), out.data_ptr(), lse.data_ptr(), status.data_ptr(), _current(dev)), _fn)
     return out, lse
 
 
@@ -553,33 +567,39 @@ def bd_attn_sink_bwd(dout, q, k, v, out, lse, seg, g: Geom, n_sink: int, status,
                      dk=None, dv=None, workspace=None, stream=None, _fn="bd_attn_sink_bwd"):
     """Gradients of bd_attn_sink_fwd: dq [B,Hq,L,D], dk / dv in k's layout (summed over each GQA group)."""
     dev = _cuda_device(q, "q")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return bd_attn_sink_bwd(dout, q, k, v, out, lse, seg, g, n_sink, status, grad_dtype, dq, dk, dv,
+                                    workspace, None, _fn)
     if grad_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("grad_dtype must be torch.float32 or torch.bfloat16")
-    for name, t in (("dout", dout), ("q", q), ("out", out)):
-        _need(t, name, torch.bfloat16, (g.B, g.Hq, g.L, g.D), dev)
-    _need(k, "k", torch.bfloat16, kv_shape(g), dev)
-    _need(v, "v", torch.bfloat16, kv_shape(g), dev)
-    _need(lse, "lse", torch.float32, (g.B, g.Hq, g.L), dev)
-    _need(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
-    _need(status, "status", torch.int32, (1,), dev)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if dq is None:
-            dq = torch.empty(g.B, g.Hq, g.L, g.D, dtype=grad_dtype, device=dev)
-        if dk is None:
-            dk = torch.empty(kv_shape(g), dtype=grad_dtype, device=dev)
-        if dv is None:
-            dv = torch.empty(kv_shape(g), dtype=grad_dtype, device=dev)
-        if workspace is None:
-            workspace = torch.empty(sink_bwd_workspace_bytes(g, n_sink), dtype=torch.uint8, device=dev)
-        _need(dq, "dq", grad_dtype, (g.B, g.Hq, g.L, g.D), dev)
-        _need(dk, "dk", grad_dtype, kv_shape(g), dev)
-        _need(dv, "dv", grad_dtype, kv_shape(g), dev)
-        _need(workspace, "workspace", torch.uint8, (sink_bwd_workspace_bytes(g, n_sink),), dev)
-        code = BD_DTYPE_BF16 if grad_dtype == torch.bfloat16 else BD_DTYPE_F32
-        _check(getattr(load(), _fn)(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(seg),
-                                    ctypes.byref(g), int(n_sink), code, _ptr(dq), _ptr(dk), _ptr(dv),
-                                    _ptr(workspace), _ptr(status), st), _fn)
+    rows, kv = (g.B, g.Hq, g.L, g.D), kv_shape(g)
+    _want(dout, "dout", torch.bfloat16, rows, dev)
+    _want(q, "q", torch.bfloat16, rows, dev)
+    _want(out, "out", torch.bfloat16, rows, dev)
+    _want(k, "k", torch.bfloat16, kv, dev)
+    _want(v, "v", torch.bfloat16, kv, dev)
+    _want(lse, "lse", torch.float32, rows[:3], dev)
+    _want(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    n = sink_bwd_workspace_bytes(g, n_sink)
+    if dq is None:
+        dq = torch.empty(rows, dtype=grad_dtype, device=dev)
+    if dk is None:
+        dk = torch.empty(kv, dtype=grad_dtype, device=dev)
+    if dv is None:
+        dv = torch.empty(kv, dtype=grad_dtype, device=dev)
+    if workspace is None:
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _want(dq, "dq", grad_dtype, rows, dev)
+    _want(dk, "dk", grad_dtype, kv, dev)
+    _want(dv, "dv", grad_dtype, kv, dev)
+    _want(workspace, "workspace", torch.uint8, (n,), dev)
+    code = BD_DTYPE_BF16 if grad_dtype == torch.bfloat16 else BD_DTYPE_F32
+    _check(getattr(load(), _fn)(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                lse.data_ptr(), seg.data_ptr(), ctypes.byref(g), int(n_sink), code, dq.data_ptr(),
+                                dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), status.data_ptr(),
+                                _current(dev)), _fn)
     return dq, dk, dv
 
 
@@ -595,27 +615,32 @@ def bd_attn_sink_bwd_main(dout, q, k, v, lse, seg, g: Geom, n_sink: int, status,
     bd_attn_bwd_prep and bd_attn_bwd_finalize. `workspace`: uint8, at least sink_bwd_workspace_bytes of every
     chunk; the other two stages take its first bwd_workspace_bytes(g) bytes."""
     dev = _cuda_device(q, "q")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return bd_attn_sink_bwd_main(dout, q, k, v, lse, seg, g, n_sink, status, workspace, dk, dv)
+    _cuda_device(dk, "dk"), _cuda_device(workspace, "workspace")
     gd = dk.dtype
     if gd not in (torch.float32, torch.bfloat16):
         raise ValueError("dk / dv must be float32 or bfloat16")
-    for name, t in (("dout", dout), ("q", q)):
-        _need(t, name, torch.bfloat16, (g.B, g.Hq, g.L, g.D), dev)
-    _need(k, "k", torch.bfloat16, kv_shape(g), dev)
-    _need(v, "v", torch.bfloat16, kv_shape(g), dev)
-    _need(lse, "lse", torch.float32, (g.B, g.Hq, g.L), dev)
-    _need(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
-    _need(dk, "dk", gd, kv_shape(g), dev)
-    _need(dv, "dv", gd, kv_shape(g), dev)
-    _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
-    if workspace.numel() < sink_bwd_workspace_bytes(g, n_sink):
-        raise ValueError(f"workspace: {workspace.numel()} bytes, {sink_bwd_workspace_bytes(g, n_sink)} needed")
-    _need(status, "status", torch.int32, (1,), dev)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        code = BD_DTYPE_BF16 if gd == torch.bfloat16 else BD_DTYPE_F32
-        _check(load().bd_attn_sink_bwd_main(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(lse), _ptr(seg),
-                                            ctypes.byref(g), int(n_sink), code, _ptr(dk), _ptr(dv), _ptr(workspace),
-                                            _ptr(status), st), "bd_attn_sink_bwd_main")
+    rows, kv = (g.B, g.Hq, g.L, g.D), kv_shape(g)
+    _want(dout, "dout", torch.bfloat16, rows, dev)
+    _want(q, "q", torch.bfloat16, rows, dev)
+    _want(k, "k", torch.bfloat16, kv, dev)
+    _want(v, "v", torch.bfloat16, kv, dev)
+    _want(lse, "lse", torch.float32, rows[:3], dev)
+    _want(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
+    _want(dk, "dk", gd, kv, dev)
+    _want(dv, "dv", gd, kv, dev)
+    _want(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    n = sink_bwd_workspace_bytes(g, n_sink)
+    if workspace.numel() < n:
+        raise ValueError(f"workspace: {workspace.numel()} bytes, {n} needed")
+    _want(status, "status", torch.int32, (1,), dev)
+    code = BD_DTYPE_BF16 if gd == torch.bfloat16 else BD_DTYPE_F32
+    _check(load().bd_attn_sink_bwd_main(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), lse.data_ptr(),
+                                        seg.data_ptr(), ctypes.byref(g), int(n_sink), code, dk.data_ptr(),
+                                        dv.data_ptr(), workspace.data_ptr(), status.data_ptr(), _current(dev)),
+           "bd_attn_sink_bwd_main")
 
 
 # ------------------------------------------------------------ paged K/V cache
@@ -634,13 +659,13 @@ def paged_decode_workspace_bytes(pg: Paged) -> int:
     return int(n)
 
 
-def _need_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev):
+def _want_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev):
     shape = (pg.n_pages, pg.Hkv, pg.page_size, pg.D)
-    _need(k_pages, "k_pages", torch.bfloat16, shape, dev)
-    _need(v_pages, "v_pages", torch.bfloat16, shape, dev)
-    _need(page_table, "page_table", torch.int32, (pg.B, pg.max_pages), dev)
-    _need(seq_lens, "seq_lens", torch.int32, (pg.B,), dev)
-    _need(status, "status", torch.int32, (1,), dev)
+    _want(k_pages, "k_pages", torch.bfloat16, shape, dev)
+    _want(v_pages, "v_pages", torch.bfloat16, shape, dev)
+    _want(page_table, "page_table", torch.int32, (pg.B, pg.max_pages), dev)
+    _want(seq_lens, "seq_lens", torch.int32, (pg.B,), dev)
+    _want(status, "status", torch.int32, (1,), dev)
 
 
 def bd_attn_paged_append(k_new, v_new, cu_new, seq_lens, page_table, pg: Paged, k_pages, v_pages, status,
@@ -648,16 +673,18 @@ def bd_attn_paged_append(k_new, v_new, cu_new, seq_lens, page_table, pg: Paged, 
     """Write k_new, v_new [T, Hkv, D] (sequence b's tokens at [cu_new[b], cu_new[b+1]), the last one at position
     seq_lens[b] - 1) into k_pages, v_pages in place."""
     dev = _cuda_device(k_pages, "k_pages")
-    _need_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev)
-    n = _cuda_device(k_new, "k_new") and k_new.shape[0]
-    _need(k_new, "k_new", torch.bfloat16, (n, pg.Hkv, pg.D), dev)
-    _need(v_new, "v_new", torch.bfloat16, (n, pg.Hkv, pg.D), dev)
-    _need(cu_new, "cu_new", torch.int32, (pg.B + 1,), dev)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        _check(load().bd_attn_paged_append(_ptr(k_new), _ptr(v_new), _ptr(cu_new), _ptr(seq_lens), _ptr(page_table),
-                                           ctypes.byref(pg), int(n), _ptr(k_pages), _ptr(v_pages), _ptr(status), st),
-               "bd_attn_paged_append")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return bd_attn_paged_append(k_new, v_new, cu_new, seq_lens, page_table, pg, k_pages, v_pages, status)
+    _want_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev)
+    _cuda_device(k_new, "k_new")
+    n = k_new.shape[0] if k_new.dim() else 0
+    _want(k_new, "k_new", torch.bfloat16, (n, pg.Hkv, pg.D), dev)
+    _want(v_new, "v_new", torch.bfloat16, (n, pg.Hkv, pg.D), dev)
+    _want(cu_new, "cu_new", torch.int32, (pg.B + 1,), dev)
+    _check(load().bd_attn_paged_append(k_new.data_ptr(), v_new.data_ptr(), cu_new.data_ptr(), seq_lens.data_ptr(),
+                                       page_table.data_ptr(), ctypes.byref(pg), n, k_pages.data_ptr(),
+                                       v_pages.data_ptr(), status.data_ptr(), _current(dev)), "bd_attn_paged_append")
 
 
 def bd_attn_paged_decode(q, k_pages, v_pages, page_table, seq_lens, pg: Paged, status, out=None, lse=None,
@@ -665,23 +692,26 @@ def bd_attn_paged_decode(q, k_pages, v_pages, page_table, seq_lens, pg: Paged, s
     """out [B, Hq, D] bf16 and lse [B, Hq] fp32 of one new token per sequence (q [B, Hq, D], at position
     seq_lens[b] - 1) over its cached keys; out 0 and lse -inf for a sequence of length 0."""
     dev = _cuda_device(q, "q")
-    _need(q, "q", torch.bfloat16, (pg.B, pg.Hq, pg.D), dev)
-    _need_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev)
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return bd_attn_paged_decode(q, k_pages, v_pages, page_table, seq_lens, pg, status, out, lse, workspace)
+    rows = (pg.B, pg.Hq, pg.D)
+    _want(q, "q", torch.bfloat16, rows, dev)
+    _want_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev)
     n = paged_decode_workspace_bytes(pg)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty(pg.B, pg.Hq, pg.D, dtype=torch.bfloat16, device=dev)
-        if lse is None:
-            lse = torch.empty(pg.B, pg.Hq, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        _need(out, "out", torch.bfloat16, (pg.B, pg.Hq, pg.D), dev)
-        _need(lse, "lse", torch.float32, (pg.B, pg.Hq), dev)
-        _need(workspace, "workspace", torch.uint8, (n,), dev)
-        _check(load().bd_attn_paged_decode(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(seq_lens),
-                                           ctypes.byref(pg), _ptr(out), _ptr(lse), _ptr(workspace), _ptr(status), st),
-               "bd_attn_paged_decode")
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(rows[:2], dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _want(out, "out", torch.bfloat16, rows, dev)
+    _want(lse, "lse", torch.float32, rows[:2], dev)
+    _want(workspace, "workspace", torch.uint8, (n,), dev)
+    _check(load().bd_attn_paged_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                                       seq_lens.data_ptr(), ctypes.byref(pg), out.data_ptr(), lse.data_ptr(),
+                                       workspace.data_ptr(), status.data_ptr(), _current(dev)),
+           "bd_attn_paged_decode")
     return out, lse
 
 

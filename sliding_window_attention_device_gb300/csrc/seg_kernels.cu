@@ -26,24 +26,14 @@ namespace bd {
 
 namespace {
 
-struct MinOp { __device__ int operator()(int a, int b) const { return a < b ? a : b; } };
-struct MaxOp { __device__ int operator()(int a, int b) const { return a > b ? a : b; } };
-struct OrOp  { __device__ int operator()(int a, int b) const { return a | b; } };
-struct AddOp { __device__ int operator()(int a, int b) const { return a + b; } };
-
-// Every thread of the block gets the reduction of `v`.
-template <class Op>
-__device__ int block_reduce(int v, Op op, int* s_red) {
+// Every thread of the block gets the sum of `v`.
+__device__ int block_add(int v, int* s_red) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  v = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
   if (lane == 0) s_red[w] = v;
   __syncthreads();
-  v = s_red[lane < nw ? lane : 0];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  return __reduce_add_sync(0xffffffffu, lane < nw ? s_red[lane] : 0);
 }
 
 // Exclusive prefix sum of `v` over the block; *total receives the sum.
@@ -58,14 +48,9 @@ __device__ int block_exclusive_scan(int v, int* s_red, int* total) {
   __syncthreads();
   if (lane == 31) s_red[w] = incl;
   __syncthreads();
-  int wpre = 0, tot = 0;
-  for (int x = 0; x < nw; ++x) {
-    const int t = s_red[x];
-    if (x < w) wpre += t;
-    tot += t;
-  }
-  *total = tot;
-  return wpre + incl - v;
+  const int x = lane < nw ? s_red[lane] : 0;  // every warp sums the warps before it
+  *total = __reduce_add_sync(0xffffffffu, x);
+  return __reduce_add_sync(0xffffffffu, lane < w ? x : 0) + incl - v;
 }
 
 }  // namespace
@@ -115,27 +100,44 @@ __device__ void sink_tile_rows(const Geom& g, const int32_t* seg, int b, int kt,
   }
 }
 
-// The local rows with a window pair in K/V tile kt: [*wb, *we).
-__device__ void window_tile_rows(const Geom& g, const int32_t* rowlo, int n_real, int kt, int* wb, int* we) {
+// The local rows with a window pair in K/V tile kt: [*wb, *we), from the tile's
+// first position on, up to where the window or the last key's document ends.
+__device__ void window_tile_rows(const Geom& g, const int32_t* seg, int b, int kt, int* wb, int* we) {
+  const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
+  const int32_t* cu_q = seg + g.off[BD_SEG_OFF_CU_Q] + b * (g.L + 1);
+  const int ro = g.row_offset, n_real = hdr[BD_SEG_N_REAL], n_seg = hdr[BD_SEG_N_SEG];
   const int s_lo = g.kv_offset + kt * kTile;
   const int s_hi = g.kv_offset + min(kt * kTile + kTile - 1, g.S_kv - 1);
-  const int i_begin = max(0, s_lo - g.row_offset);
-  // first row in [i_begin, n_real) whose lo exceeds s_hi
-  int a = i_begin, e = n_real;
-  while (a < e) {
-    const int mid = (a + e) >> 1;
-    if (row_lo_window(rowlo[mid], g.row_offset + mid, g.window) > s_hi) e = mid; else a = mid + 1;
+  const int i_begin = max(0, s_lo - ro);
+  int end = n_real;
+  if (n_seg == 0 || s_hi < hdr[BD_SEG_S_FIRST]) {
+    end = 0;
+  } else if (s_hi < ro + n_real) {  // the document of s_hi ends the rows
+    int k = 0;
+    if (s_hi >= ro) {
+      int a = 0, e = n_seg - 1;
+      while (a < e) {
+        const int mid = (a + e + 1) >> 1;
+        if (ro + cu_q[mid] <= s_hi) a = mid; else e = mid - 1;
+      }
+      k = a;
+    }
+    end = cu_q[k + 1];
   }
-  *wb = i_begin < a ? i_begin : 0;
-  *we = i_begin < a ? a : 0;
+  if (g.window > 0) end = static_cast<int>(min(static_cast<long long>(end), static_cast<long long>(s_hi) + g.window - ro));
+  *wb = i_begin < end ? i_begin : 0;
+  *we = i_begin < end ? end : 0;
 }
 
-// One CTA per batch row.
+// One CTA per batch row; each warp takes a contiguous piece of it, 32 positions
+// at a time, so that runs are found with ballots.
 __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restrict__ doc, Geom g,
                                                          int32_t* __restrict__ seg, int32_t* status, int kv_chunk) {
   pdl_begin();
   __shared__ int s_red[32];
+  __shared__ int s_w[4][32];
   const int b = blockIdx.x, tid = threadIdx.x, nthr = blockDim.x;
+  const int lane = tid & 31, warp = tid >> 5, n_warps = nthr >> 5;
   const int ro = g.row_offset, L = g.L;
   const int32_t* row = doc + static_cast<size_t>(b) * g.S_full;
   int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
@@ -143,99 +145,95 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
   int32_t* cu_k = seg + g.off[BD_SEG_OFF_CU_K] + b * (L + 1);
   int32_t* rowlo = seg + g.off[BD_SEG_OFF_ROW_LO] + b * L;
 
-  // Layout over the whole row: ids >= 0, no document after padding.
-  int bad = 0;
+  // One pass over the whole row: ids >= 0 and no document after padding; the
+  // shard's first padding row (L if none); the start of the run that holds the
+  // shard's first position; whether ids ever fall from one document to the next.
+  int flags = 0, first_pad = L, s_first = 0;  // flags: 1 bad layout, 2 falling ids
+  {
+    const int piece = cdiv(cdiv(g.S_full, 32), n_warps) * 32;
+    const int e = min(g.S_full, (warp + 1) * piece);
 #pragma unroll 8
-  for (int p = tid; p < g.S_full; p += nthr) {
-    const int c = row[p];
-    if (c < 0 || (p > 0 && c != 0 && row[p - 1] == 0)) bad = 1;
-  }
-  bad = block_reduce(bad, OrOp(), s_red);
-
-  // n_real: the first padding row of the shard (L if none).
-  int first_pad = L;
-  for (int i = tid; i < L; i += nthr)
-    if (row[ro + i] == 0) {
-      first_pad = i;
-      break;
+    for (int p = warp * piece + lane; p < e; p += 32) {
+      const int c = row[p], prev = p > 0 ? row[p - 1] : c;
+      if (c < 0 || (c != 0 && prev == 0 && p > 0)) flags |= 1;
+      if (c != 0 && prev != 0 && c < prev) flags |= 2;
+      if (c == 0 && p >= ro && p < ro + L) first_pad = min(first_pad, p - ro);
+      if (p <= ro && c != prev) s_first = p;
     }
-  const int n_real = block_reduce(first_pad, MinOp(), s_red);
-
-  // Segment starts: local row 0 and every row whose id differs from the previous
-  // one, compacted in order with a ballot + block scan.
-  int n_seg = 0;
-  for (int c0 = 0; c0 < n_real; c0 += nthr) {
-    const int i = c0 + tid;
-    const int f = (i < n_real) && (i == 0 || row[ro + i] != row[ro + i - 1]);
-    int tot;
-    const int pos = block_exclusive_scan(f, s_red, &tot);
-    if (f) cu_q[n_seg + pos] = i;
-    n_seg += tot;
   }
+  flags = __reduce_or_sync(0xffffffffu, flags);
+  first_pad = __reduce_min_sync(0xffffffffu, first_pad);
+  s_first = __reduce_max_sync(0xffffffffu, s_first);
+  if (lane == 0) {
+    s_w[0][warp] = flags;
+    s_w[1][warp] = first_pad;
+    s_w[2][warp] = s_first;
+  }
+  __syncthreads();
+  flags = __reduce_or_sync(0xffffffffu, lane < n_warps ? s_w[0][lane] : 0);
+  const int n_real = __reduce_min_sync(0xffffffffu, lane < n_warps ? s_w[1][lane] : L);
+  s_first = __reduce_max_sync(0xffffffffu, lane < n_warps ? s_w[2][lane] : 0);
+  if (n_real == 0) s_first = ro;
+  int bad = flags & 1;
 
-  // Document start of the first segment: scan left from the shard start.
-  int s_first = ro;
-  if (n_real > 0) {
-    const int id0 = row[ro];
-    int found = -1;
-    for (int c1 = ro; c1 > 0; c1 -= nthr) {
-      const int p = c1 - 1 - tid;
-      const int f = (p >= 0 && row[p] != id0) ? p : -1;
-      const int m = block_reduce(f, MaxOp(), s_red);
-      if (m >= 0) {
-        found = m;
-        break;
-      }
+  // Segments: they start at local row 0 and at every real row whose id differs
+  // from the previous one. First the pieces' counts and last starts, then their
+  // places; each row's document start is the last start at or before it.
+  const int piece = cdiv(cdiv(n_real, 32), n_warps) * 32;
+  const int r0 = min(n_real, warp * piece), r1 = min(n_real, r0 + piece);
+  auto starts = [&](int i0) -> unsigned {
+    const int i = i0 + lane;
+    return __ballot_sync(0xffffffffu, i < r1 && (i == 0 || row[ro + i] != row[ro + i - 1]));
+  };
+  int count = 0, last = -1;
+#pragma unroll 4
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const unsigned m = starts(i0);
+    count += __popc(m);
+    if (m) last = i0 + 31 - __clz(m);
+  }
+  if (lane == 0) {
+    s_w[3][warp] = count;
+    s_red[warp] = last;
+  }
+  __syncthreads();
+  const int cnt_l = lane < n_warps ? s_w[3][lane] : 0;
+  const int n_seg = __reduce_add_sync(0xffffffffu, cnt_l);
+  int at = __reduce_add_sync(0xffffffffu, lane < warp ? cnt_l : 0);
+  int cur = __reduce_max_sync(0xffffffffu, lane < warp ? s_red[lane] : -1);  // last start before this piece
+#pragma unroll 4
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const unsigned m = starts(i0);
+    const int i = i0 + lane;
+    const unsigned upto = m & (0xffffffffu >> (31 - lane));
+    if (i < r1) {
+      if (m >> lane & 1u) cu_q[at + __popc(upto) - 1] = i;
+      const int st = upto ? i0 + 31 - __clz(upto) : cur;  // 0: the straddling document
+      rowlo[i] = st == 0 ? s_first : ro + st;
     }
-    s_first = found + 1;
+    at += __popc(m);
+    if (m) cur = i0 + 31 - __clz(m);
   }
+  for (int i = n_real + tid; i < L; i += nthr) rowlo[i] = -1;  // padding rows
   if (tid == 0) cu_q[n_seg] = n_real;
   __syncthreads();  // cu_q visible to the whole block
 
-  // Each local document id must not occur before its own run. Fast path: ids
-  // increase from segment to segment and the first one exceeds every id before
-  // the straddle. Otherwise check every segment exactly.
-  if (n_seg > 0) {
-    int m0 = INT_MIN;
-#pragma unroll 8
-    for (int p = tid; p < s_first; p += nthr) m0 = max(m0, row[p]);
-    m0 = block_reduce(m0, MaxOp(), s_red);
-    int fast_ok = 1;
-    for (int k = tid; k < n_seg; k += nthr) {
+  // Each local document id must not occur before its own run. Ids that never
+  // fall from one document to the next cannot; otherwise check every segment.
+  if (flags & 2) {
+    int dup = 0;
+    for (int k = 0; k < n_seg && !dup; ++k) {
       const int idk = row[ro + cu_q[k]];
-      const int prev = (k == 0) ? m0 : row[ro + cu_q[k - 1]];
-      if (!(idk > prev)) fast_ok = 0;
+      const int st = (k == 0) ? s_first : ro + cu_q[k];
+      int hit = 0;
+      for (int p = tid; p < st; p += nthr)
+        if (row[p] == idk) {
+          hit = 1;
+          break;
+        }
+      dup = __syncthreads_or(hit);
     }
-    fast_ok = block_reduce(fast_ok, MinOp(), s_red);
-    if (!fast_ok) {
-      int dup = 0;
-      for (int k = 0; k < n_seg && !dup; ++k) {
-        const int idk = row[ro + cu_q[k]];
-        const int st = (k == 0) ? s_first : ro + cu_q[k];
-        int hit = 0;
-        for (int p = tid; p < st; p += nthr)
-          if (row[p] == idk) {
-            hit = 1;
-            break;
-          }
-        dup = block_reduce(hit, OrOp(), s_red);
-      }
-      bad |= dup;
-    }
-  }
-
-  // Document start of every local row (-1 on padding rows).
-  for (int i = tid; i < L; i += nthr) {
-    int v = -1;
-    if (i < n_real) {
-      int lo = 0, hi = n_seg - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu_q[mid] <= i) lo = mid; else hi = mid - 1;
-      }
-      v = (lo == 0) ? s_first : ro + cu_q[lo];
-    }
-    rowlo[i] = v;
+    bad |= dup;
   }
 
   // cu_k and the maxima.
@@ -250,9 +248,20 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
     mk = max(mk, sk);
     if (k >= 1) mt = max(mt, sq);
   }
-  mq = block_reduce(mq, MaxOp(), s_red);
-  mk = block_reduce(mk, MaxOp(), s_red);
-  mt = block_reduce(mt, MaxOp(), s_red);
+  mq = __reduce_max_sync(0xffffffffu, mq);
+  mk = __reduce_max_sync(0xffffffffu, mk);
+  mt = __reduce_max_sync(0xffffffffu, mt);
+  __syncthreads();
+  if (lane == 0) {
+    s_w[0][warp] = mq;
+    s_w[1][warp] = mk;
+    s_w[2][warp] = mt;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  mq = __reduce_max_sync(0xffffffffu, lane < n_warps ? s_w[0][lane] : 0);
+  mk = __reduce_max_sync(0xffffffffu, lane < n_warps ? s_w[1][lane] : 0);
+  mt = __reduce_max_sync(0xffffffffu, lane < n_warps ? s_w[2][lane] : 0);
 
   if (tid == 0) {
     cu_k[n_seg] = real_end - s_first;
@@ -302,9 +311,8 @@ __device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int n
   // units of a tile: rows [beg, end0), then pieces of `span` up to end; returns their number
   auto ranges = [&](int item, int* beg, int* end0, int* end, int* rbase) -> int {
     const int b = item / g.nkt, kt = item % g.nkt;
-    const int n_real = seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL];
     int wb, we, sb, se;
-    window_tile_rows(g, seg + g.off[BD_SEG_OFF_ROW_LO] + b * g.L, n_real, kt, &wb, &we);
+    window_tile_rows(g, seg, b, kt, &wb, &we);
     sink_tile_rows(g, seg, b, kt, &sb, &se, rbase);
     if (wb >= we) {
       wb = sb;
@@ -328,7 +336,7 @@ __device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int n
       atomicAdd(&s_hist[x == 0 ? bin_of(beg, end0) : bin_of(end0 + (x - 1) * span, min(end, end0 + x * span))], 1);
     n_units += n;
   }
-  n_units = block_reduce(n_units, AddOp(), s_red);
+  n_units = block_add(n_units, s_red);
   int carry = 0;  // exclusive scan of the histogram, in chunks of blockDim
   for (int c0 = 0; c0 < nbins; c0 += nthr) {
     const int x = c0 + tid;
@@ -374,7 +382,7 @@ __device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int n
     n_sums += tot_sums;
     n_slots += tot_slots;
   }
-  over = block_reduce(over ? 1 : 0, OrOp(), s_red) != 0;
+  over = __syncthreads_or(over ? 1 : 0) != 0;
   if (tid == 0) {
     // an overflow would be an error of the capacities: nothing is run on the table
     hdr[0] = over ? -1 : n_units;
@@ -385,35 +393,56 @@ __device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int n
   }
 }
 
-// CTA 0 classifies every tile of every batch row and builds the two
-// longest-first work lists; CTA 1, launched for sink tables, builds the
-// backward's units, which need nothing of CTA 0's. Dynamic shared memory: (nbins) ints of histogram.
+// Items (n of them, key(item) in [0, nbins)) in descending order of their keys:
+// a counting sort, the order within a key left open.
+template <class Key>
+__device__ void list_longest_first(int n, int nbins, Key key, int32_t* out, int* s_hist, int* s_red) {
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  for (int x = tid; x < nbins; x += nthr) s_hist[x] = 0;
+  __syncthreads();
+  for (int it = tid; it < n; it += nthr) atomicAdd(&s_hist[nbins - 1 - min(key(it), nbins - 1)], 1);
+  __syncthreads();
+  int carry = 0;  // exclusive scan of the histogram, in chunks of blockDim
+  for (int c0 = 0; c0 < nbins; c0 += nthr) {
+    const int x = c0 + tid;
+    const int v = x < nbins ? s_hist[x] : 0;
+    int tot;
+    const int ex = block_exclusive_scan(v, s_red, &tot);
+    if (x < nbins) s_hist[x] = carry + ex;
+    carry += tot;
+  }
+  __syncthreads();
+  for (int it = tid; it < n; it += nthr) out[atomicAdd(&s_hist[nbins - 1 - min(key(it), nbins - 1)], 1)] = it;
+}
+
+// CTA 0 classifies the q tiles (their K/V tiles, the full ones, the forward's
+// longest-first list), CTA 1 the K/V tiles (their q rows, the backward's list);
+// CTA 2, launched for sink tables, lists the backward's units. None needs
+// anything of the others'. Dynamic shared memory: nbins ints of histogram.
 __global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restrict__ seg, int nbins,
                                                         int32_t* status) {
   pdl_begin();
   extern __shared__ int s_hist[];
   __shared__ int s_red[32];
-  if (blockIdx.x == 1) {
+  if (blockIdx.x == 2) {
     build_sink_units(g, seg, nbins, status, s_hist, s_red);
     return;
   }
   const int tid = threadIdx.x, nthr = blockDim.x;
-  const int ro = g.row_offset, L = g.L, W = g.window;
-  int n_full = 0, n_part = 0, n_kv_att = 0;
+  const int ro = g.row_offset, W = g.window;
+  int32_t* counts = seg + g.off[BD_SEG_OFF_COUNTS];
 
-  for (int b = 0; b < g.B; ++b) {
-    const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
-    const int32_t* rowlo = seg + g.off[BD_SEG_OFF_ROW_LO] + b * L;
-    int32_t* qk = seg + g.off[BD_SEG_OFF_QT_KRANGE] + b * g.nqt * 2;
-    int32_t* kq = seg + g.off[BD_SEG_OFF_KT_QRANGE] + b * g.nkt * 2;
-    int32_t* bits = seg + g.off[BD_SEG_OFF_FULL_BITS] + b * g.nqt * g.nkw;
-    const int n_real = hdr[BD_SEG_N_REAL];
-
+  if (blockIdx.x == 0) {
     // Per q tile: the range of K/V tiles and which of them are full.
-    for (int qt = tid; qt < g.nqt; qt += nthr) {
-      const int first = qt * kTile;
-      int kt_lo = 0, kt_hi = -1;
-      for (int w = 0; w < g.nkw; ++w) bits[qt * g.nkw + w] = 0;
+    int n_full = 0, n_part = 0;
+    const int n_items = g.B * g.nqt;
+    for (int item = tid; item < n_items; item += nthr) {
+      const int b = item / g.nqt, qt = item % g.nqt, first = qt * kTile;
+      const int n_real = seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL];
+      const int32_t* rowlo = seg + g.off[BD_SEG_OFF_ROW_LO] + b * g.L;
+      int32_t* qk = seg + g.off[BD_SEG_OFF_QT_KRANGE] + 2 * item;
+      int32_t* bits = seg + g.off[BD_SEG_OFF_FULL_BITS] + item * g.nkw;
+      int kt_lo = 0, kt_hi = -1, f_lo = 0, f_hi = -1;  // f: the full tiles, an interval
       if (first < n_real) {
         const int last = min(first + kTile - 1, n_real - 1);
         const int j_lo = max(row_lo_window(rowlo[first], ro + first, W) - g.kv_offset, 0);
@@ -421,120 +450,98 @@ __global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restr
         if (j_lo <= j_hi) {
           kt_lo = j_lo / kTile;
           kt_hi = j_hi / kTile;
-          const bool all_real = first + kTile - 1 < n_real;
-          const int lo_last = row_lo_window(rowlo[last], ro + last, W);
-          const int hi_first = ro + first;
-          uint32_t word = 0;
-          int cur_w = kt_lo >> 5;
-          for (int kt = kt_lo; kt <= kt_hi; ++kt) {
-            if ((kt >> 5) != cur_w) {
-              bits[qt * g.nkw + cur_w] = static_cast<int32_t>(word);
-              word = 0;
-              cur_w = kt >> 5;
-            }
-            const int s0 = g.kv_offset + kt * kTile;
-            const bool full = all_real && lo_last <= s0 && s0 + kTile - 1 <= hi_first &&
-                              kt * kTile + kTile - 1 < g.S_kv;
-            if (full) {
-              word |= 1u << (kt & 31);
-              ++n_full;
-            } else {
-              ++n_part;
-            }
+          if (first + kTile - 1 < n_real) {  // every row is real
+            // the tile starts at or behind the last row's first key and ends at or before the first row
+            const int a = max(row_lo_window(rowlo[last], ro + last, W) - g.kv_offset, 0);
+            const int e = min(ro + first - g.kv_offset + 1, g.S_kv);  // keys [a, e)
+            f_lo = max(kt_lo, cdiv(a, kTile));
+            f_hi = min(kt_hi, (e > 0 ? e / kTile : 0) - 1);
           }
-          bits[qt * g.nkw + cur_w] = static_cast<int32_t>(word);
+          const int full = max(0, f_hi - f_lo + 1);
+          n_full += full;
+          n_part += kt_hi - kt_lo + 1 - full;
         }
       }
-      qk[2 * qt] = kt_lo;
-      qk[2 * qt + 1] = kt_hi;
+      for (int w = 0; w < g.nkw; ++w) {
+        const int x = max(f_lo - 32 * w, 0), y = min(f_hi - 32 * w, 31);
+        bits[w] = x <= y ? static_cast<int32_t>((0xffffffffu >> (31 - y)) & (0xffffffffu << x)) : 0;
+      }
+      qk[0] = kt_lo;
+      qk[1] = kt_hi;
     }
-
-    // Per K/V tile: the local q rows whose allowed interval meets it.
-    for (int kt = tid; kt < g.nkt; kt += nthr) {
-      int wb, we, sb, se, rbase;
-      window_tile_rows(g, rowlo, n_real, kt, &wb, &we);
+    n_full = block_add(n_full, s_red);
+    n_part = block_add(n_part, s_red);
+    if (tid == 0) {
+      counts[0] = n_full;
+      counts[1] = n_part;
+      counts[2] = g.B * g.nqt * g.nkt - n_full - n_part;
+      for (int x = 4; x < 8; ++x) counts[x] = 0;
+    }
+    __syncthreads();  // ranges written above are read below by other threads
+    list_longest_first(n_items, nbins, [&](int item) {
+      const int32_t* qk = seg + g.off[BD_SEG_OFF_QT_KRANGE] + item * 2;
+      int key = qk[1] >= qk[0] ? qk[1] - qk[0] + 1 : 0;
       if (g.n_sink > 0) {
-        sink_tile_rows(g, seg, b, kt, &sb, &se, &rbase);
-        if (sb < se) {
-          wb = wb < we ? min(wb, sb) : sb;
-          we = max(we, se);
-        }
+        const int b = item / g.nqt;
+        int x0, nx, col[2];
+        sink_passes(g, seg, b, item % g.nqt, seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL], &x0,
+                    &nx, col);
+        key += nx;
       }
-      kq[2 * kt] = wb;
-      kq[2 * kt + 1] = we;
-      n_kv_att += wb < we ? 1 : 0;
-    }
+      return key;
+    }, seg + g.off[BD_SEG_OFF_FWD_WORK], s_hist, s_red);
+    return;
   }
-  n_full = block_reduce(n_full, AddOp(), s_red);
-  n_part = block_reduce(n_part, AddOp(), s_red);
-  n_kv_att = block_reduce(n_kv_att, AddOp(), s_red);
-  if (tid == 0) {
-    int32_t* counts = seg + g.off[BD_SEG_OFF_COUNTS];
-    counts[0] = n_full;
-    counts[1] = n_part;
-    counts[2] = g.B * g.nqt * g.nkt - n_full - n_part;
-    counts[3] = n_kv_att;  // these K/V tiles lead the backward work list
-    for (int x = 4; x < 8; ++x) counts[x] = 0;
-  }
-  __syncthreads();  // ranges written above are read below by other threads
 
-  // Longest-first work lists (counting sort on the work estimate, descending).
-  for (int list = 0; list < 2; ++list) {
-    const int n_items = list == 0 ? g.B * g.nqt : g.B * g.nkt;
-    int32_t* out = seg + g.off[list == 0 ? BD_SEG_OFF_FWD_WORK : BD_SEG_OFF_BWD_WORK];
-    for (int x = tid; x < nbins; x += nthr) s_hist[x] = 0;
-    __syncthreads();
-    auto key_of = [&](int item) -> int {
-      int key;
-      if (list == 0) {
-        const int32_t* qk = seg + g.off[BD_SEG_OFF_QT_KRANGE] + item * 2;
-        key = qk[1] >= qk[0] ? qk[1] - qk[0] + 1 : 0;
-        if (g.n_sink > 0) {
-          const int b = item / g.nqt;
-          int x0, nx, col[2];
-          sink_passes(g, seg, b, item % g.nqt, seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL], &x0,
-                      &nx, col);
-          key += nx;
-        }
-      } else {
-        const int32_t* kq = seg + g.off[BD_SEG_OFF_KT_QRANGE] + item * 2;
-        key = kq[1] > kq[0] ? (kq[1] - 1) / kBwdQ - kq[0] / kBwdQ + 1 : 0;
+  // Per K/V tile: the local q rows whose allowed keys meet it.
+  int n_kv_att = 0;
+  const int n_items = g.B * g.nkt;
+  for (int item = tid; item < n_items; item += nthr) {
+    const int b = item / g.nkt, kt = item % g.nkt;
+    int32_t* kq = seg + g.off[BD_SEG_OFF_KT_QRANGE] + 2 * item;
+    int wb, we, sb, se, rbase;
+    window_tile_rows(g, seg, b, kt, &wb, &we);
+    if (g.n_sink > 0) {
+      sink_tile_rows(g, seg, b, kt, &sb, &se, &rbase);
+      if (sb < se) {
+        wb = wb < we ? min(wb, sb) : sb;
+        we = max(we, se);
       }
-      return min(key, nbins - 1);
-    };
-    for (int it = tid; it < n_items; it += nthr) atomicAdd(&s_hist[nbins - 1 - key_of(it)], 1);
-    __syncthreads();
-    // exclusive scan of the histogram, in chunks of blockDim
-    int carry = 0;
-    for (int c0 = 0; c0 < nbins; c0 += nthr) {
-      const int x = c0 + tid;
-      const int v = x < nbins ? s_hist[x] : 0;
-      int tot;
-      const int ex = block_exclusive_scan(v, s_red, &tot);
-      __syncthreads();
-      if (x < nbins) s_hist[x] = carry + ex;
-      carry += tot;
-      __syncthreads();
     }
-    for (int it = tid; it < n_items; it += nthr) {
-      const int pos = atomicAdd(&s_hist[nbins - 1 - key_of(it)], 1);
-      out[pos] = it;
-    }
-    __syncthreads();
+    kq[0] = wb;
+    kq[1] = we;
+    n_kv_att += wb < we ? 1 : 0;
   }
+  n_kv_att = block_add(n_kv_att, s_red);
+  if (tid == 0) counts[3] = n_kv_att;  // these K/V tiles lead the backward work list
+  __syncthreads();
+  list_longest_first(n_items, nbins, [&](int item) {
+    const int32_t* kq = seg + g.off[BD_SEG_OFF_KT_QRANGE] + item * 2;
+    return kq[1] > kq[0] ? (kq[1] - 1) / kBwdQ - kq[0] / kBwdQ + 1 : 0;
+  }, seg + g.off[BD_SEG_OFF_BWD_WORK], s_hist, s_red);
 }
 
 cudaError_t launch_seg_build(const int32_t* doc, const Geom& g, int32_t* seg, int32_t* status, cudaStream_t st,
                              int kv_chunk) {
-  if (const cudaError_t le = launch_pdl(seg_build_kernel, dim3(g.B), dim3(1024), 0, st, doc, g, seg, status, kv_chunk);
+  // blocks no wider than their work: a barrier of 8 warps is cheaper than one of 32
+  auto threads = [](long long items) {
+    int n = 128;
+    while (n < 1024 && n < items) n *= 2;
+    return dim3(n);
+  };
+  if (const cudaError_t le = launch_pdl(seg_build_kernel, dim3(g.B), threads(g.S_full / 8), 0, st, doc, g, seg, status,
+                                        kv_chunk);
       le != cudaSuccess) return le;
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // histogram bins of the work-list sort (48 KB of shared memory at most)
   int nbins = (g.nkt > cdiv(g.L, kBwdQ) ? g.nkt : cdiv(g.L, kBwdQ)) + 1;
   if (nbins > 12288) nbins = 12288;
-  if (const cudaError_t le = launch_pdl(classify_kernel, dim3(g.sink_tab ? 2 : 1), dim3(1024),
-      static_cast<size_t>(nbins) * 4, st, g, seg, nbins, status); le != cudaSuccess) return le;
+  const int widest = g.nkt > g.nqt ? g.nkt : g.nqt;
+  if (const cudaError_t le = launch_pdl(classify_kernel, dim3(g.sink_tab ? 3 : 2),
+                                        threads(static_cast<long long>(g.B) * widest),
+                                        static_cast<size_t>(nbins) * 4, st, g, seg, nbins, status);
+      le != cudaSuccess) return le;
   return cudaGetLastError();
 }
 
