@@ -409,7 +409,7 @@ int bd_attn_paged_append(const void* k_new, const void* v_new, const int32_t* cu
  * sequence of length 0 gets out = 0, lse = -inf. Results are bitwise
  * reproducible for the same lengths. workspace:
  * bd_attn_paged_decode_workspace_bytes bytes, 16-byte aligned, not shared by
- * calls that may overlap. */
+ * calls that may overlap; NULL will do where that size is 16 (no row is split). */
 size_t bd_attn_paged_decode_workspace_bytes(const bd_paged* g);
 int bd_attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
                          const int32_t* seq_lens, const bd_paged* g, void* out, float* lse, void* workspace,

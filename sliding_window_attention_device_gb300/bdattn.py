@@ -469,11 +469,14 @@ def read_seg(seg: torch.Tensor, g: Geom) -> dict:
 SINK_MAX = 128  # BD_SINK_MAX
 
 
-def _want(t, name: str, dtype, shape, dev):
-    """_need, with one test when nothing is wrong."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
-            and t.is_cuda and t.is_contiguous()):
-        _need(t, name, dtype, shape, dev)
+def _want(dev, *tensors):
+    """_need for every (tensor, name, dtype, shape); one test each when nothing is wrong, as small calls are
+    bound by the host."""
+    i = dev.index
+    for t, name, dtype, shape in tensors:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == i and t.shape == shape
+                and t.is_contiguous()):
+            _need(t, name, dtype, shape, dev)
 
 
 def _cuda_device(t, name):
@@ -492,8 +495,15 @@ def _elsewhere(dev, stream):
     return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
+# the current stream's handle without making a Stream object of it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _current(dev) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+    return torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(dev.index)
+
+
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def sink_seg_bytes(g: Geom, n_sink: int) -> int:
@@ -524,9 +534,7 @@ def bd_attn_sink_seg_build(doc_ids: torch.Tensor, g: Geom, n_sink: int, kv_chunk
         seg = torch.empty(n, dtype=torch.int32, device=dev)
     if status is None:
         status = new_status(dev)
-    _want(doc_ids, "doc_ids", torch.int32, (g.B, g.S_full), dev)
-    _want(seg, "seg", torch.int32, (n,), dev)
-    _want(status, "status", torch.int32, (1,), dev)
+    _want(dev, (doc_ids, "doc_ids", _I32, (g.B, g.S_full)), (seg, "seg", _I32, (n,)), (status, "status", _I32, (1,)))
     _check(load().bd_attn_sink_seg_build(doc_ids.data_ptr(), ctypes.byref(g), int(n_sink), int(bool(kv_chunk)),
                                          seg.data_ptr(), status.data_ptr(), _current(dev)), "bd_attn_sink_seg_build")
     return seg, status
@@ -540,17 +548,13 @@ def bd_attn_sink_fwd(q, k, v, seg, g: Geom, n_sink: int, status, out=None, lse=N
         with ctx:
             return bd_attn_sink_fwd(q, k, v, seg, g, n_sink, status, out, lse, None, _fn)
     rows, kv = (g.B, g.Hq, g.L, g.D), kv_shape(g)
-    _want(q, "q", torch.bfloat16, rows, dev)
-    _want(k, "k", torch.bfloat16, kv, dev)
-    _want(v, "v", torch.bfloat16, kv, dev)
-    _want(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
-    _want(status, "status", torch.int32, (1,), dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty(rows, dtype=_BF16, device=dev)
     if lse is None:
-        lse = torch.empty(rows[:3], dtype=torch.float32, device=dev)
-    _want(out, "out", torch.bfloat16, rows, dev)
-    _want(lse, "lse", torch.float32, rows[:3], dev)
+        lse = torch.empty(rows[:3], dtype=_F32, device=dev)
+    _want(dev, (q, "q", _BF16, rows), (k, "k", _BF16, kv), (v, "v", _BF16, kv),
+          (seg, "seg", _I32, (sink_seg_bytes(g, n_sink) // 4,)), (status, "status", _I32, (1,)),
+          (out, "out", _BF16, rows), (lse, "lse", _F32, rows[:3]))
     _check(getattr(load(), _fn)(q.data_ptr(), k.data_ptr(), v.data_ptr(), seg.data_ptr(), ctypes.byref(g),
                                 int(n_sink), out.data_ptr(), lse.data_ptr(), status.data_ptr(), _current(dev)), _fn)
     return out, lse
@@ -574,14 +578,6 @@ def bd_attn_sink_bwd(dout, q, k, v, out, lse, seg, g: Geom, n_sink: int, status,
     if grad_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("grad_dtype must be torch.float32 or torch.bfloat16")
     rows, kv = (g.B, g.Hq, g.L, g.D), kv_shape(g)
-    _want(dout, "dout", torch.bfloat16, rows, dev)
-    _want(q, "q", torch.bfloat16, rows, dev)
-    _want(out, "out", torch.bfloat16, rows, dev)
-    _want(k, "k", torch.bfloat16, kv, dev)
-    _want(v, "v", torch.bfloat16, kv, dev)
-    _want(lse, "lse", torch.float32, rows[:3], dev)
-    _want(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
-    _want(status, "status", torch.int32, (1,), dev)
     n = sink_bwd_workspace_bytes(g, n_sink)
     if dq is None:
         dq = torch.empty(rows, dtype=grad_dtype, device=dev)
@@ -591,10 +587,10 @@ def bd_attn_sink_bwd(dout, q, k, v, out, lse, seg, g: Geom, n_sink: int, status,
         dv = torch.empty(kv, dtype=grad_dtype, device=dev)
     if workspace is None:
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    _want(dq, "dq", grad_dtype, rows, dev)
-    _want(dk, "dk", grad_dtype, kv, dev)
-    _want(dv, "dv", grad_dtype, kv, dev)
-    _want(workspace, "workspace", torch.uint8, (n,), dev)
+    _want(dev, (dout, "dout", _BF16, rows), (q, "q", _BF16, rows), (out, "out", _BF16, rows), (k, "k", _BF16, kv),
+          (v, "v", _BF16, kv), (lse, "lse", _F32, rows[:3]), (seg, "seg", _I32, (sink_seg_bytes(g, n_sink) // 4,)),
+          (status, "status", _I32, (1,)), (dq, "dq", grad_dtype, rows), (dk, "dk", grad_dtype, kv),
+          (dv, "dv", grad_dtype, kv), (workspace, "workspace", _U8, (n,)))
     code = BD_DTYPE_BF16 if grad_dtype == torch.bfloat16 else BD_DTYPE_F32
     _check(getattr(load(), _fn)(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                 lse.data_ptr(), seg.data_ptr(), ctypes.byref(g), int(n_sink), code, dq.data_ptr(),
@@ -623,19 +619,12 @@ def bd_attn_sink_bwd_main(dout, q, k, v, lse, seg, g: Geom, n_sink: int, status,
     if gd not in (torch.float32, torch.bfloat16):
         raise ValueError("dk / dv must be float32 or bfloat16")
     rows, kv = (g.B, g.Hq, g.L, g.D), kv_shape(g)
-    _want(dout, "dout", torch.bfloat16, rows, dev)
-    _want(q, "q", torch.bfloat16, rows, dev)
-    _want(k, "k", torch.bfloat16, kv, dev)
-    _want(v, "v", torch.bfloat16, kv, dev)
-    _want(lse, "lse", torch.float32, rows[:3], dev)
-    _want(seg, "seg", torch.int32, (sink_seg_bytes(g, n_sink) // 4,), dev)
-    _want(dk, "dk", gd, kv, dev)
-    _want(dv, "dv", gd, kv, dev)
-    _want(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    _want(dev, (dout, "dout", _BF16, rows), (q, "q", _BF16, rows), (k, "k", _BF16, kv), (v, "v", _BF16, kv),
+          (lse, "lse", _F32, rows[:3]), (seg, "seg", _I32, (sink_seg_bytes(g, n_sink) // 4,)), (dk, "dk", gd, kv),
+          (dv, "dv", gd, kv), (workspace, "workspace", _U8, (workspace.numel(),)), (status, "status", _I32, (1,)))
     n = sink_bwd_workspace_bytes(g, n_sink)
     if workspace.numel() < n:
         raise ValueError(f"workspace: {workspace.numel()} bytes, {n} needed")
-    _want(status, "status", torch.int32, (1,), dev)
     code = BD_DTYPE_BF16 if gd == torch.bfloat16 else BD_DTYPE_F32
     _check(load().bd_attn_sink_bwd_main(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), lse.data_ptr(),
                                         seg.data_ptr(), ctypes.byref(g), int(n_sink), code, dk.data_ptr(),
@@ -659,15 +648,6 @@ def paged_decode_workspace_bytes(pg: Paged) -> int:
     return int(n)
 
 
-def _want_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev):
-    shape = (pg.n_pages, pg.Hkv, pg.page_size, pg.D)
-    _want(k_pages, "k_pages", torch.bfloat16, shape, dev)
-    _want(v_pages, "v_pages", torch.bfloat16, shape, dev)
-    _want(page_table, "page_table", torch.int32, (pg.B, pg.max_pages), dev)
-    _want(seq_lens, "seq_lens", torch.int32, (pg.B,), dev)
-    _want(status, "status", torch.int32, (1,), dev)
-
-
 def bd_attn_paged_append(k_new, v_new, cu_new, seq_lens, page_table, pg: Paged, k_pages, v_pages, status,
                          stream=None):
     """Write k_new, v_new [T, Hkv, D] (sequence b's tokens at [cu_new[b], cu_new[b+1]), the last one at position
@@ -676,12 +656,12 @@ def bd_attn_paged_append(k_new, v_new, cu_new, seq_lens, page_table, pg: Paged, 
     if (ctx := _elsewhere(dev, stream)) is not None:
         with ctx:
             return bd_attn_paged_append(k_new, v_new, cu_new, seq_lens, page_table, pg, k_pages, v_pages, status)
-    _want_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev)
     _cuda_device(k_new, "k_new")
-    n = k_new.shape[0] if k_new.dim() else 0
-    _want(k_new, "k_new", torch.bfloat16, (n, pg.Hkv, pg.D), dev)
-    _want(v_new, "v_new", torch.bfloat16, (n, pg.Hkv, pg.D), dev)
-    _want(cu_new, "cu_new", torch.int32, (pg.B + 1,), dev)
+    n, B = k_new.shape[0] if k_new.dim() else 0, pg.B
+    cache, new = (pg.n_pages, pg.Hkv, pg.page_size, pg.D), (n, pg.Hkv, pg.D)
+    _want(dev, (k_new, "k_new", _BF16, new), (v_new, "v_new", _BF16, new), (cu_new, "cu_new", _I32, (B + 1,)),
+          (seq_lens, "seq_lens", _I32, (B,)), (page_table, "page_table", _I32, (B, pg.max_pages)),
+          (k_pages, "k_pages", _BF16, cache), (v_pages, "v_pages", _BF16, cache), (status, "status", _I32, (1,)))
     _check(load().bd_attn_paged_append(k_new.data_ptr(), v_new.data_ptr(), cu_new.data_ptr(), seq_lens.data_ptr(),
                                        page_table.data_ptr(), ctypes.byref(pg), n, k_pages.data_ptr(),
                                        v_pages.data_ptr(), status.data_ptr(), _current(dev)), "bd_attn_paged_append")
@@ -695,23 +675,23 @@ def bd_attn_paged_decode(q, k_pages, v_pages, page_table, seq_lens, pg: Paged, s
     if (ctx := _elsewhere(dev, stream)) is not None:
         with ctx:
             return bd_attn_paged_decode(q, k_pages, v_pages, page_table, seq_lens, pg, status, out, lse, workspace)
-    rows = (pg.B, pg.Hq, pg.D)
-    _want(q, "q", torch.bfloat16, rows, dev)
-    _want_cache(k_pages, v_pages, page_table, seq_lens, status, pg, dev)
+    rows, cache = (pg.B, pg.Hq, pg.D), (pg.n_pages, pg.Hkv, pg.page_size, pg.D)
     n = paged_decode_workspace_bytes(pg)
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty(rows, dtype=_BF16, device=dev)
     if lse is None:
-        lse = torch.empty(rows[:2], dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    _want(out, "out", torch.bfloat16, rows, dev)
-    _want(lse, "lse", torch.float32, rows[:2], dev)
-    _want(workspace, "workspace", torch.uint8, (n,), dev)
+        lse = torch.empty(rows[:2], dtype=_F32, device=dev)
+    if workspace is None and n > 16:  # 16: the call needs none
+        workspace = torch.empty(n, dtype=_U8, device=dev)
+    _want(dev, (q, "q", _BF16, rows), (k_pages, "k_pages", _BF16, cache), (v_pages, "v_pages", _BF16, cache),
+          (page_table, "page_table", _I32, (rows[0], pg.max_pages)), (seq_lens, "seq_lens", _I32, rows[:1]),
+          (status, "status", _I32, (1,)), (out, "out", _BF16, rows), (lse, "lse", _F32, rows[:2]))
+    if workspace is not None:
+        _want(dev, (workspace, "workspace", _U8, (n,)))
     _check(load().bd_attn_paged_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
                                        seq_lens.data_ptr(), ctypes.byref(pg), out.data_ptr(), lse.data_ptr(),
-                                       workspace.data_ptr(), status.data_ptr(), _current(dev)),
-           "bd_attn_paged_decode")
+                                       workspace.data_ptr() if workspace is not None else None, status.data_ptr(),
+                                       _current(dev)), "bd_attn_paged_decode")
     return out, lse
 
 

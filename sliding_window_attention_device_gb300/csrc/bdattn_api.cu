@@ -690,8 +690,8 @@ int bd_attn_paged_decode(const void* q, const void* k_pages, const void* v_pages
                          int32_t* status, bd_stream_t stream) {
   PagedGeom g;
   if (int rc = to_paged(gi, &g)) return rc;
-  if (!q || !k_pages || !v_pages || !page_table || !seq_lens || !out || !lse || !workspace || !status)
-    return BD_ERR_ARG;
+  if (!q || !k_pages || !v_pages || !page_table || !seq_lens || !out || !lse || !status) return BD_ERR_ARG;
+  if (!workspace && !dec_whole_rows(g)) return BD_ERR_ARG;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))
     return BD_ERR_ARG;
   if (int rc = check_device()) return rc;

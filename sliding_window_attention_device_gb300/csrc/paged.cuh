@@ -33,6 +33,17 @@ constexpr int kDecKeys = 16;
 constexpr int kDecSms = 152;
 __host__ __device__ inline int dec_ctas(int D) { return D <= 256 ? 2 * kDecSms : kDecSms; }
 __host__ __device__ inline int dec_head_tiles(int D, int G) { return D <= 256 && G > 8 ? 2 : 1; }
+// Whether a CTA takes whole rows: no sequence can show a new token many keys,
+// or not very many and there are rows for most SMs.
+__host__ __device__ inline bool dec_whole_rows(const PagedGeom& g) {
+  long long n = static_cast<long long>(g.max_pages) * g.page_size;
+  if (g.window > 0 && n > static_cast<long long>(g.window) + g.n_sink) n = static_cast<long long>(g.window) + g.n_sink;
+  if (g.D > 256) return n <= 128;
+  const int heads = 8 * dec_head_tiles(g.D, g.G);
+  const long long rows = static_cast<long long>(g.B) * g.Hkv * ((g.G + heads - 1) / heads);
+  return n <= 512 || (n <= 2048 && rows >= 128);
+}
+constexpr size_t kDecNoWorkspace = 16;  // what the size query answers then: nothing is kept there
 // Workspace: per CTA a descriptor (8 ints), then two partials of (m, l) and O
 // for each of its heads.
 __host__ __device__ inline size_t dec_desc_bytes(int D) { return static_cast<size_t>(dec_ctas(D)) * 32; }

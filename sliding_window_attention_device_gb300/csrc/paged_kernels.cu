@@ -110,6 +110,8 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int3
 //   warp's softmax needs no other warp, and no step waits for a barrier. (The
 //   tensor rate is not what bounds this: one mma covers 512 bytes of cache.)
 //   Softmax statistics and O in fp32; P is rounded to bf16 for the product.
+// Where no sequence can have more than kDecWholeKeys visible keys, a CTA takes
+// a whole row instead: no line, no second kernel.
 // At the end of a row's piece the warps join through shared memory. A row
 // inside one CTA is written at once; of a row cut over CTAs each leaves (m, l,
 // O) in the workspace, and paged_join_kernel adds them in CTA order.
@@ -184,9 +186,9 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kDecWarps * 32)
     paged_decode_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k_pages,
                         const __nv_bfloat16* __restrict__ v_pages, const int32_t* __restrict__ page_table,
-                        const int32_t* __restrict__ seq_lens, const PagedGeom g, __nv_bfloat16* __restrict__ out,
-                        float* __restrict__ lse, DecDesc* __restrict__ desc, float* __restrict__ part,
-                        int32_t* status) {
+                        const int32_t* __restrict__ seq_lens, const PagedGeom g, int whole_rows,
+                        __nv_bfloat16* __restrict__ out, float* __restrict__ lse, DecDesc* __restrict__ desc,
+                        float* __restrict__ part, int32_t* status) {
   pdl_begin();
   using C = DecCfg<D, NT>;
   constexpr int kThreads = kDecWarps * 32, kHeads = C::kHeads, kKs = D / 16;
@@ -197,61 +199,86 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_hb = (g.G + kHeads - 1) / kHeads, rows_b = g.Hkv * n_hb;
 
-  // ---- this CTA's piece of the line of steps
-  // thread t sums the steps of sequences [t * span, (t + 1) * span)
-  const int span = (g.B + kThreads - 1) / kThreads;
-  long long mine = 0;
   bool bad = false;
-  for (int b = tid * span; b < min(g.B, (tid + 1) * span); ++b) {
+  int b = 0;
+  long long per = 1, at = 0, end = 0, in_b = 0;  // steps [at, end) of the line; step of sequence b that `at` is
+  if (whole_rows) {
+    // ---- one row per CTA
+    b = blockIdx.x / rows_b;
+    const int row = blockIdx.x % rows_b;
     const Visible v = visible_keys(g, seq_lens, b, &bad);
-    mine += static_cast<long long>((v.n + kDecKeys - 1) / kDecKeys) * rows_b;
-  }
-  if (bad) atomicOr(status, BD_STATUS_BOUNDS);
-  if (tid == 0) s_skip = *reinterpret_cast<const volatile int*>(status) != 0;
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = incl - mine;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
-  }
-  if (tid == 0) desc[blockIdx.x].last_cta = -1;
-  if (s_skip) return;
-  // equal pieces, but no fewer than one step per warp
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < kDecWarps) per = kDecWarps;
-  const long long begin = per * blockIdx.x, end = min(begin + per, total);
-
-  // sequences without a visible key: zeros and -inf, shared out over the CTAs
-  for (int b = blockIdx.x; b < g.B; b += gridDim.x) {
-    bool x = false;
-    if (visible_keys(g, seq_lens, b, &x).n > 0) continue;
-    uint4* o4 = reinterpret_cast<uint4*>(out + static_cast<size_t>(b) * g.Hq * D);
-    for (int i = tid; i < g.Hq * (D / 8); i += kThreads) o4[i] = make_uint4(0, 0, 0, 0);
-    for (int i = tid; i < g.Hq; i += kThreads) lse[static_cast<size_t>(b) * g.Hq + i] = -INFINITY;
-  }
-  if (begin >= end) return;
-  // the thread whose sequences hold step `begin` finds the one
-  if (begin >= before && begin < before + mine) {
-    long long at = before;
-    int b = tid * span;
-    for (;; ++b) {
-      const Visible v = visible_keys(g, seq_lens, b, &bad);
-      const long long n = static_cast<long long>((v.n + kDecKeys - 1) / kDecKeys) * rows_b;
-      if (begin < at + n) break;
-      at += n;
+    if (bad && tid == 0) atomicOr(status, BD_STATUS_BOUNDS);
+    if (*reinterpret_cast<const volatile int*>(status) != 0) return;
+    const int steps = (v.n + kDecKeys - 1) / kDecKeys;
+    if (steps == 0) {
+      const int heads = min(kHeads, g.G - row % n_hb * kHeads);
+      const size_t r0 = static_cast<size_t>(b) * g.Hq + row / n_hb * g.G + row % n_hb * kHeads;
+      uint4* o4 = reinterpret_cast<uint4*>(out + r0 * D);
+      for (int i = tid; i < heads * (D / 8); i += kThreads) o4[i] = make_uint4(0, 0, 0, 0);
+      if (tid < heads) lse[r0 + tid] = -INFINITY;
+      return;
     }
-    s_b = b;
-    s_at = begin - at;
+    in_b = static_cast<long long>(row) * steps;
+    end = steps;
+  } else {
+    // ---- an equal piece of the line of steps
+    // thread t sums the steps of sequences [t * span, (t + 1) * span)
+    const int span = (g.B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int x = tid * span; x < min(g.B, (tid + 1) * span); ++x) {
+      const Visible v = visible_keys(g, seq_lens, x, &bad);
+      mine += static_cast<long long>((v.n + kDecKeys - 1) / kDecKeys) * rows_b;
+    }
+    if (bad) atomicOr(status, BD_STATUS_BOUNDS);
+    if (tid == 0) s_skip = *reinterpret_cast<const volatile int*>(status) != 0;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      if (w < warp) before += s_sum[w];
+      total += s_sum[w];
+    }
+    if (tid == 0) desc[blockIdx.x].last_cta = -1;
+    if (s_skip) return;
+    // no fewer than one step per warp
+    per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < kDecWarps) per = kDecWarps;
+    at = per * blockIdx.x;
+    end = min(at + per, total);
+
+    // sequences without a visible key: zeros and -inf, shared out over the CTAs
+    for (int x = blockIdx.x; x < g.B; x += gridDim.x) {
+      bool y = false;
+      if (visible_keys(g, seq_lens, x, &y).n > 0) continue;
+      uint4* o4 = reinterpret_cast<uint4*>(out + static_cast<size_t>(x) * g.Hq * D);
+      for (int i = tid; i < g.Hq * (D / 8); i += kThreads) o4[i] = make_uint4(0, 0, 0, 0);
+      for (int i = tid; i < g.Hq; i += kThreads) lse[static_cast<size_t>(x) * g.Hq + i] = -INFINITY;
+    }
+    if (at >= end) return;
+    // the thread whose sequences hold the first step finds the one
+    if (at >= before && at < before + mine) {
+      long long sum = before;
+      int x = tid * span;
+      for (;; ++x) {
+        const Visible v = visible_keys(g, seq_lens, x, &bad);
+        const long long n = static_cast<long long>((v.n + kDecKeys - 1) / kDecKeys) * rows_b;
+        if (at < sum + n) break;
+        sum += n;
+      }
+      s_b = x;
+      s_at = at - sum;
+    }
+    __syncthreads();
+    b = s_b;
+    in_b = s_at;
   }
-  __syncthreads();
 
   uint8_t* ring = smem + warp * C::kItems * C::kItem;
   const uint32_t ring_a = smem_u32(ring);
@@ -259,10 +286,8 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   float* ml = reinterpret_cast<float*>(smem + C::kRing + C::kQBytes);  // [warp][head] m, l
   const float sl2 = g.scale * 1.4426950408889634f;
 
-  int b = s_b;
-  long long in_b = s_at;  // step within the sequence's rows
   bool first_piece = true;
-  for (long long at = begin; at < end;) {
+  while (at < end) {
     const Visible v = visible_keys(g, seq_lens, b, &bad);
     const int steps = (v.n + kDecKeys - 1) / kDecKeys;
     if (in_b >= static_cast<long long>(steps) * rows_b) {
@@ -276,7 +301,49 @@ __global__ void __launch_bounds__(kDecWarps * 32)
     const int heads = min(kHeads, g.G - hb * kHeads);  // query heads of this row
     const int h0 = hk * g.G + hb * kHeads;
 
-    // Q^T fragments: head lane / 4 of each 8, d pairs of each 16
+    // ---- this warp's steps t0 + warp, t0 + warp + 4, ...
+    const int n_mine = t1 - t0 > warp ? (t1 - t0 - warp + kDecWarps - 1) / kDecWarps : 0;
+    // the page and place of key lane % 16 of my i-th step (-1: no such key); the
+    // page is loaded a step before it is looked at
+    auto page_at = [&](int i, int* off) -> int {
+      const int x = (t0 + warp + i * kDecWarps) * kDecKeys + (lane & 15);
+      if (i >= n_mine || x >= v.n) {
+        *off = -1;
+        return 0;
+      }
+      return page_of(g, page_table, b, x < v.ns ? x : v.lo + (x - v.ns), off);
+    };
+    int off_next, page_next = page_at(0, &off_next);
+    uint32_t row_cur = 0xffffffffu;  // cache row of that key of the step being copied (0xffffffff: none)
+    // item y: K (even) or V (odd) of my step y / 2
+    auto issue = [&](int y) {
+      if (y < 2 * n_mine) {
+        if ((y & 1) == 0) {
+          row_cur = 0xffffffffu;
+          if (off_next >= 0) {
+            if (page_next >= 0 && page_next < g.n_pages) row_cur = page_row(g, page_next, hk, off_next);
+            else atomicOr(status, BD_STATUS_BOUNDS);
+          }
+          page_next = page_at((y >> 1) + 1, &off_next);
+        }
+        const __nv_bfloat16* base = (y & 1) ? v_pages : k_pages;
+        const uint32_t dst = ring_a + (y % C::kItems) * C::kItem;
+        constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+#pragma unroll
+        for (int x = 0; x < kDecKeys * kPieces / 32; ++x) {
+          const int piece = (x * 32 + lane) % kPieces, r = (x * 32 + lane) / kPieces;
+          const uint32_t src = __shfl_sync(0xffffffffu, row_cur, r);
+          const bool ok = src != 0xffffffffu;
+          cp_async16(dst + r * (D * 2) + ((piece ^ (r & 7)) << 4),
+                     base + static_cast<size_t>(ok ? src : 0u) * D + piece * 8, ok);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll 1
+    for (int y = 0; y < C::kItems - 1; ++y) issue(y);
+
+    // Q^T fragments (behind the first copies): head lane / 4 of each 8, d pairs of each 16
     uint32_t qf[C::kQSmem ? 1 : NT][C::kQSmem ? 1 : kKs][2];
     const __nv_bfloat16* qb = q + (static_cast<size_t>(b) * g.Hq + h0) * D;
     if constexpr (C::kQSmem) {
@@ -299,46 +366,6 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       }
     }
 
-    // ---- this warp's steps t0 + warp, t0 + warp + 4, ...
-    const int n_mine = t1 - t0 > warp ? (t1 - t0 - warp + kDecWarps - 1) / kDecWarps : 0;
-    // cache row of key lane % 16 of my i-th step (0xffffffff: none)
-    auto rows_of = [&](int i) -> uint32_t {
-      if (i >= n_mine) return 0xffffffffu;
-      const int x = (t0 + warp + i * kDecWarps) * kDecKeys + (lane & 15);
-      if (x >= v.n) return 0xffffffffu;
-      int off;
-      const int page = page_of(g, page_table, b, x < v.ns ? x : v.lo + (x - v.ns), &off);
-      if (page < 0 || page >= g.n_pages) {
-        atomicOr(status, BD_STATUS_BOUNDS);
-        return 0xffffffffu;
-      }
-      return page_row(g, page, hk, off);
-    };
-    uint32_t row_cur = 0xffffffffu, row_next = rows_of(0);
-    // item y: K (even) or V (odd) of my step y / 2
-    auto issue = [&](int y) {
-      if (y < 2 * n_mine) {
-        if ((y & 1) == 0) {
-          row_cur = row_next;
-          row_next = rows_of((y >> 1) + 1);
-        }
-        const __nv_bfloat16* base = (y & 1) ? v_pages : k_pages;
-        const uint32_t dst = ring_a + (y % C::kItems) * C::kItem;
-        constexpr int kPieces = D / 8;  // 16-byte pieces of a row
-#pragma unroll
-        for (int x = 0; x < kDecKeys * kPieces / 32; ++x) {
-          const int piece = (x * 32 + lane) % kPieces, r = (x * 32 + lane) / kPieces;
-          const uint32_t src = __shfl_sync(0xffffffffu, row_cur, r);
-          const bool ok = src != 0xffffffffu;
-          cp_async16(dst + r * (D * 2) + ((piece ^ (r & 7)) << 4),
-                     base + static_cast<size_t>(ok ? src : 0u) * D + piece * 8, ok);
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll 1
-    for (int y = 0; y < C::kItems - 1; ++y) issue(y);
-
     float acc[NT][kKs][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -352,15 +379,17 @@ __global__ void __launch_bounds__(kDecWarps * 32)
     }
 #pragma unroll 1
     for (int i = 0; i < n_mine; ++i) {
-      // K item: S^T = K Q^T
+      // K item: S^T = K Q^T, in kChains sums so that no product waits for the one before
       cp_async_wait<C::kItems - 2>();
       __syncwarp();
-      issue(2 * i + C::kItems - 1);
-      float s[NT][4];
+      constexpr int kChains = kKs >= 8 ? 4 : 2;
+      float sc[kChains][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int c = 0; c < kChains; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[c][nt][e] = 0.f;
       {
         const uint32_t a0 = ring_a + (2 * i % C::kItems) * C::kItem;
         const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -373,33 +402,38 @@ __global__ void __launch_bounds__(kDecWarps * 32)
           for (int nt = 0; nt < NT; ++nt) {
             if constexpr (C::kQSmem) {
               const uint2 bq = qs[(nt * kKs + ks) * 32 + lane];
-              mma16816(s[nt], a, bq.x, bq.y);
+              mma16816(sc[ks % kChains][nt], a, bq.x, bq.y);
             } else {
-              mma16816(s[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+              mma16816(sc[ks % kChains][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
             }
           }
         }
       }
-      // online softmax over the 16 keys; this thread: keys lane / 4 and + 8, heads 2 (lane % 4) and + 1
+      issue(2 * i + C::kItems - 1);
+      // online softmax over the 16 keys; this thread: keys lane / 4 and + 8, heads 2 (lane % 4) and + 1.
+      // The running maximum is raised, and O and the sum rescaled, only when a
+      // score passes it by 2^8.
       const int x0 = (t0 + warp + i * kDecWarps) * kDecKeys + (lane >> 2);
       const bool in0 = x0 < v.n, in1 = x0 + 8 < v.n;
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float x[4];
-        x[0] = in0 ? s[nt][0] * sl2 : -INFINITY;
-        x[1] = in0 ? s[nt][1] * sl2 : -INFINITY;
-        x[2] = in1 ? s[nt][2] * sl2 : -INFINITY;
-        x[3] = in1 ? s[nt][3] * sl2 : -INFINITY;
-        float m0 = fmaxf(x[0], x[2]), m1 = fmaxf(x[1], x[3]);
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+        for (int e = 0; e < 4; ++e) {
+          float sum = sc[0][nt][e] + sc[1][nt][e];
+          if constexpr (kChains == 4) sum += sc[2][nt][e] + sc[3][nt][e];
+          x[e] = (e < 2 ? in0 : in1) ? sum * sl2 : -INFINITY;
         }
-        m0 = fmaxf(m0, m[nt][0]);
-        m1 = fmaxf(m1, m[nt][1]);
-        if (__any_sync(0xffffffffu, m0 > m[nt][0] || m1 > m[nt][1])) {
+        float m0 = fmaxf(x[0], x[2]), m1 = fmaxf(x[1], x[3]);
+        if (__any_sync(0xffffffffu, m0 > m[nt][0] + 8.0f || m1 > m[nt][1] + 8.0f)) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+          }
+          m0 = fmaxf(m0, m[nt][0]);
+          m1 = fmaxf(m1, m[nt][1]);
           const float al0 = fast_exp2(m[nt][0] - m0), al1 = fast_exp2(m[nt][1] - m1);
           l[nt][0] *= al0;
           l[nt][1] *= al1;
@@ -413,8 +447,8 @@ __global__ void __launch_bounds__(kDecWarps * 32)
           m[nt][0] = m0;
           m[nt][1] = m1;
         }
-        const float p0 = fast_exp2(x[0] - m0), p1 = fast_exp2(x[1] - m1);
-        const float p2 = fast_exp2(x[2] - m0), p3 = fast_exp2(x[3] - m1);
+        const float p0 = fast_exp2(x[0] - m[nt][0]), p1 = fast_exp2(x[1] - m[nt][1]);
+        const float p2 = fast_exp2(x[2] - m[nt][0]), p3 = fast_exp2(x[3] - m[nt][1]);
         l[nt][0] += p0 + p2;
         l[nt][1] += p1 + p3;
         pb[nt][0] = transpose8x8(pack_bf16x2(p0, p1));  // keys along the product's inner side
@@ -423,7 +457,6 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       // V item: O^T += V^T P^T
       cp_async_wait<C::kItems - 2>();
       __syncwarp();
-      issue(2 * i + C::kItems);
       {
         const uint32_t a0 = ring_a + ((2 * i + 1) % C::kItems) * C::kItem;
         const int r = (lane & 7) + (lane >> 4) * 8;
@@ -436,6 +469,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
           for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][ks], a, pb[nt][0], pb[nt][1]);
         }
       }
+      issue(2 * i + C::kItems);
     }
     cp_async_wait<0>();
     __syncwarp();
@@ -510,71 +544,109 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   }
 }
 
-// A row cut over CTAs: log-sum-exp weights over their partials, in CTA order.
-// One CTA per (CTA the row starts in, head); each of its warps takes every
-// fourth partial.
+// A row cut over CTAs: log-sum-exp weights over their partials. One CTA per (CTA
+// the row starts in, head); each of its warps runs over every eighth partial,
+// eight loads in flight, with a running maximum, and the warps are added in
+// order: the same bits in every run.
+constexpr int kJoinWarps = 8;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedGeom g, const DecDesc* __restrict__ desc,
-                                                         const float* __restrict__ part,
-                                                         __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                                                         const int32_t* status) {
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    paged_join_kernel(const PagedGeom g, int heads, const DecDesc* __restrict__ desc, const float* __restrict__ part,
+                      __nv_bfloat16* __restrict__ out, float* __restrict__ lse, const int32_t* status) {
   pdl_begin();
   constexpr int kHeads = 8 * NT, kVec = (D + 127) / 128;  // float4 per lane
-  const int c0 = blockIdx.x / kHeads, h = blockIdx.x % kHeads;
+  constexpr int kBatch = D <= 128 ? 8 : D <= 256 ? 4 : 2;
+  const int c0 = blockIdx.x / heads, h = blockIdx.x % heads;
   const DecDesc d = desc[c0];
   if (*reinterpret_cast<const volatile int*>(status) != 0 || d.last_cta < 0 || h >= g.G - d.hb * kHeads) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ float s_m[4], s_l[4];
-  __shared__ float4 s_o[4][D / 4];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  __shared__ float4 s_o[kJoinWarps][D / 4];
   const int n = d.last_cta - c0 + 1;
   auto part_of = [&](int i) {
     return part + static_cast<size_t>(i == 0 ? d.slot : 2 * (c0 + i)) * dec_part_floats(D, kHeads);
   };
-  float mm = -INFINITY;
-  for (int i = tid; i < n; i += 128) mm = fmaxf(mm, part_of(i)[h * 4]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-  if (lane == 0) s_m[warp] = mm;
-  __syncthreads();
-  mm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f;
+  float mm = -INFINITY, ll = 0.f;
   float4 o[kVec];
 #pragma unroll
   for (int e = 0; e < kVec; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = warp; i < n; i += 4) {
-    const float* p = part_of(i);
-    const float f = fast_exp2(p[h * 4] - base);
-    ll = fmaf(f, p[h * 4 + 1], ll);
+  for (int i0 = warp; i0 < n; i0 += kJoinWarps * kBatch) {
+    float pm[kBatch], pl[kBatch], bm = mm;
+    float4 y[kBatch][kVec];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kJoinWarps;
+      pm[k] = -INFINITY;
+      pl[k] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) y[k][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const float* p = part_of(i);
+        const float2 x = *reinterpret_cast<const float2*>(p + h * 4);
+        pm[k] = x.x;
+        pl[k] = x.y;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+          if (e * 128 + lane * 4 < D)
+            y[k][e] = *reinterpret_cast<const float4*>(p + kHeads * 4 + h * D + e * 128 + lane * 4);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, pm[k]);
+    const float base = bm == -INFINITY ? 0.f : bm, f0 = fast_exp2(mm - base);
+    mm = bm;
+    ll *= f0;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-      if (e * 128 + lane * 4 < D) {
-        const float4 y = *reinterpret_cast<const float4*>(p + kHeads * 4 + h * D + e * 128 + lane * 4);
-        o[e].x = fmaf(f, y.x, o[e].x);
-        o[e].y = fmaf(f, y.y, o[e].y);
-        o[e].z = fmaf(f, y.z, o[e].z);
-        o[e].w = fmaf(f, y.w, o[e].w);
+      o[e].x *= f0;
+      o[e].y *= f0;
+      o[e].z *= f0;
+      o[e].w *= f0;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float f = fast_exp2(pm[k] - base);
+      ll = fmaf(f, pl[k], ll);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        o[e].x = fmaf(f, y[k][e].x, o[e].x);
+        o[e].y = fmaf(f, y[k][e].y, o[e].y);
+        o[e].z = fmaf(f, y[k][e].z, o[e].z);
+        o[e].w = fmaf(f, y[k][e].w, o[e].w);
       }
     }
   }
-  if (lane == 0) s_l[warp] = ll;
+  if (lane == 0) {
+    s_m[warp] = mm;
+    s_l[warp] = ll;
+  }
 #pragma unroll
   for (int e = 0; e < kVec; ++e)
     if (e * 128 + lane * 4 < D) s_o[warp][e * 32 + lane] = o[e];
   __syncthreads();
-  ll = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  mm = s_m[0];
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) mm = fmaxf(mm, s_m[w]);
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float f[kJoinWarps];
+  ll = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    f[w] = fast_exp2(s_m[w] - base);
+    ll = fmaf(f[w], s_l[w], ll);
+  }
   const float inv = ll > 0.f ? 1.0f / ll : 0.f;
   const size_t r = static_cast<size_t>(d.b) * g.Hq + d.hk * g.G + d.hb * kHeads + h;
-  for (int x = tid; x < D / 4; x += 128) {
-    float4 a = s_o[0][x];
+  for (int x = tid; x < D / 4; x += kJoinWarps * 32) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 1; w < 4; ++w) {
+    for (int w = 0; w < kJoinWarps; ++w) {
       const float4 y = s_o[w][x];
-      a.x += y.x;
-      a.y += y.y;
-      a.z += y.z;
-      a.w += y.w;
+      a.x = fmaf(f[w], y.x, a.x);
+      a.y = fmaf(f[w], y.y, a.y);
+      a.z = fmaf(f[w], y.z, a.z);
+      a.w = fmaf(f[w], y.w, a.w);
     }
     *reinterpret_cast<uint2*>(out + r * D + x * 4) =
         make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
@@ -593,16 +665,19 @@ cudaError_t launch_decode_dn(const void* q, const void* k_pages, const void* v_p
   if (e != cudaSuccess) return e;
   DecDesc* desc = static_cast<DecDesc*>(workspace);
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dec_desc_bytes(D));
-  const unsigned ctas = static_cast<unsigned>(dec_ctas(D));
+  const bool whole = dec_whole_rows(g);
+  const int n_hb = (g.G + C::kHeads - 1) / C::kHeads, heads = g.G < C::kHeads ? g.G : C::kHeads;
+  const unsigned ctas = static_cast<unsigned>(whole ? g.B * g.Hkv * n_hb : dec_ctas(D));
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
   if (const cudaError_t le = launch_pdl(kern, dim3(ctas), dim3(kDecWarps * 32), C::kSmem, st,
                                         static_cast<const __nv_bfloat16*>(q),
                                         static_cast<const __nv_bfloat16*>(k_pages),
-                                        static_cast<const __nv_bfloat16*>(v_pages), page_table, seq_lens, g, o, lse,
-                                        desc, part, status);
+                                        static_cast<const __nv_bfloat16*>(v_pages), page_table, seq_lens, g,
+                                        static_cast<int>(whole), o, lse, desc, part, status);
       le != cudaSuccess)
     return le;
-  if (const cudaError_t le = launch_pdl(paged_join_kernel<D, NT>, dim3(ctas * C::kHeads), dim3(128), 0, st, g,
+  if (whole) return cudaGetLastError();
+  if (const cudaError_t le = launch_pdl(paged_join_kernel<D, NT>, dim3(ctas * heads), dim3(kJoinWarps * 32), 0, st, g, heads,
                                         static_cast<const DecDesc*>(desc), static_cast<const float*>(part), o, lse,
                                         static_cast<const int32_t*>(status));
       le != cudaSuccess)
@@ -612,6 +687,7 @@ cudaError_t launch_decode_dn(const void* q, const void* k_pages, const void* v_p
 }  // namespace
 
 size_t paged_decode_workspace_bytes(const PagedGeom& g) {
+  if (dec_whole_rows(g)) return kDecNoWorkspace;
   return dec_desc_bytes(g.D) + 2 * static_cast<size_t>(dec_ctas(g.D)) *
                                    dec_part_floats(g.D, 8 * dec_head_tiles(g.D, g.G)) * 4;
 }

@@ -340,7 +340,7 @@ def test_refusals():
         with pytest.raises(ValueError):
             D(*args, pg, status)
     with pytest.raises(ValueError):
-        D(q, k, k, table, lens, pg, status, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        D(q, k, k, table, lens, pg, status, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         D(q, k, k, table, lens, bdattn.paged_geom(2, 4, 2, 96, 8, 16, 4), status)
     for args in ((new.float(), new, cu), (new, new[:2], cu), (new, new, cu[:2]), (new.cpu(), new, cu)):

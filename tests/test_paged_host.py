@@ -21,7 +21,7 @@ def test_struct_matches_header():
     assert re.findall(r"\b(?:int|float)\s+(\w+);", fields) == [n for n, _ in bdattn.Paged._fields_]
 
 
-BASE = dict(B=4, Hq=8, Hkv=2, D=128, n_pages=100, page_size=16, max_pages=20)
+BASE = dict(B=4, Hq=8, Hkv=2, D=128, n_pages=100, page_size=16, max_pages=200)
 
 
 @pytest.mark.parametrize("bad", [
