@@ -346,3 +346,68 @@ def test_refusals():
     for args in ((new.float(), new, cu), (new, new[:2], cu), (new, new, cu[:2]), (new.cpu(), new, cu)):
         with pytest.raises(ValueError):
             A(*args, lens, table, pg, k, k, status)
+
+
+def test_cache_beyond_32_bit_offsets():
+    """Pages whose elements lie past 2^32: appended to, and read back by decode."""
+    D, page, Hkv, n_pages = 128, 16, 2, (1 << 20) + 40  # 2^32 elements and a little, 8.6 GB each
+    k = torch.empty(n_pages, Hkv, page, D, dtype=torch.bfloat16, device=DEV)
+    v = torch.empty_like(k)
+    lens = [70, 33]
+    ids = [[n_pages - 1, 3, 1 << 19, n_pages - 7, (1 << 19) + 1], [n_pages - 2, 0, n_pages - 30]]
+    table = torch.full((2, 5), -1, dtype=torch.int32)
+    table[0, :5], table[1, :3] = torch.tensor(ids[0]), torch.tensor(ids[1])
+    gen = torch.Generator().manual_seed(0)
+    kn, vn = (torch.randn(sum(lens), Hkv, D, generator=gen).bfloat16() for _ in range(2))
+    q = torch.randn(2, 4, D, generator=gen).bfloat16()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    pg = bdattn.paged_geom(2, 4, Hkv, D, n_pages, page, 5)
+    status = bdattn.new_status(DEV)
+    bdattn.bd_attn_paged_append(kn.to(DEV), vn.to(DEV), i32(0, 70, 103), i32(*lens), table.to(DEV), pg, k, v, status)
+    for b, s in enumerate((0, 70)):
+        for pos in range(lens[b]):
+            assert torch.equal(k[ids[b][pos // page], :, pos % page].cpu(), kn[s + pos])
+    out, lse = bdattn.bd_attn_paged_decode(q.to(DEV), k, v, table.to(DEV), i32(*lens), pg, status)
+    assert int(status.item()) == 0
+    check(out, lse, plain(q, [(kn[:70], vn[:70]), (kn[70:], vn[70:])], 0, 0))
+
+
+def test_shared_pages():
+    """Two sequences on one prefix, and one place of the batch listed twice: pages are only read."""
+    table, k, v, rows = cache([64, 20], 2, 128, 16, seed=5)
+    n_pages = k.shape[0]
+    t2 = torch.full((3, 4), -1, dtype=torch.int32)
+    t2[0], t2[1, :4], t2[2, :2] = table[0], table[0], table[1, :2]
+    t2[1, 2:] = table[1, :2]  # the first 32 tokens of sequence 0, then sequence 1's
+    second = tuple(torch.cat([a[:32], c]) for a, c in zip(rows[0], rows[1]))
+    q = torch.randn(3, 4, 128, generator=torch.Generator().manual_seed(8)).bfloat16()
+    pg = bdattn.paged_geom(3, 4, 2, 128, n_pages, 16, 4)
+    status = bdattn.new_status(DEV)
+    out, lse = bdattn.bd_attn_paged_decode(q.to(DEV), k.to(DEV), v.to(DEV), t2.to(DEV),
+                                           torch.tensor([64, 52, 20], dtype=torch.int32, device=DEV), pg, status)
+    assert int(status.item()) == 0
+    check(out, lse, plain(q, [rows[0], second, rows[1]], 0, 0))
+
+
+def test_decode_joins_a_running_result():
+    """A cache in two parts: each part's (out, lse) merged by bd_attn_merge is the whole's."""
+    D, Hq, Hkv, n = 128, 4, 2, 500
+    table, k, v, rows = cache([n], Hkv, D, 16, seed=6)
+    q = torch.randn(1, Hq, D, generator=torch.Generator().manual_seed(9)).bfloat16().to(DEV)
+    k, v, table = k.to(DEV), v.to(DEV), table.to(DEV)
+    status = bdattn.new_status(DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    cut = 12  # pages
+    res = []
+    for t, m in ((table[:, :cut].contiguous(), cut * 16), (table[:, cut:].contiguous(), n - cut * 16)):
+        pg = bdattn.paged_geom(1, Hq, Hkv, D, k.shape[0], 16, t.shape[1])
+        res.append(bdattn.bd_attn_paged_decode(q, k, v, t, i32(m), pg, status))
+    g = bdattn.geom(1, Hq, Hkv, D, 1, 1, 0, 0, 1)
+    out, lse = (x.reshape(1, Hq, 1, -1).contiguous() for x in res[0])
+    oc, lc = (x.reshape(1, Hq, 1, -1).contiguous() for x in res[1])
+    lse, lc = lse.reshape(1, Hq, 1), lc.reshape(1, Hq, 1)
+    bdattn.bd_attn_merge(out, lse, oc, lc, g, status)
+    assert int(status.item()) == 0
+    o, l, e, r2 = plain(q.cpu(), rows, 0, 0)
+    # the parts' roundings and the merge's own: three bounds of one
+    check(out.reshape(1, Hq, D), lse.reshape(1, Hq), (o, l, 3 * e, 9 * r2))

@@ -291,3 +291,36 @@ def test_refusals():
         bdattn.bd_attn_sink_bwd(q, q, k, k, q, torch.zeros(1, 2, 256, device=dev), seg, g, 4, status, torch.float16)
     with pytest.raises(ValueError):
         bdattn.bd_attn_sink_fwd_merge(q, k, k, seg, g, 4, status, None, None)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_scale(D):
+    """A softmax scale of its own: the reference with q scaled by scale / D^-0.5 (a power of two, so exactly)."""
+    c = make_case(W(1, 2, 1, D, 500, 2, ("explicit", (40, 420), 40), 60), 1, seed=8)
+    g = gpu_geom(c)
+    g.scale = 0.5 * D ** -0.5
+    dev = torch.device("cuda")
+    q, k, v, do = (c[x].to(dev) for x in ("q", "k", "v", "do"))
+    seg, status = bdattn.bd_attn_sink_seg_build(torch.from_numpy(c["doc"]).to(dev), g, 4)
+    out, lse = bdattn.bd_attn_sink_fwd(q, k, v, seg, g, 4, status)
+    dq, dk, dv = bdattn.bd_attn_sink_bwd(do, q, k, v, out, lse, seg, g, 4, status)
+    assert int(status.item()) == 0
+    cc = dict(c)
+    cc["q"] = (c["q"].float() * 0.5).bfloat16()
+    ref = reference(cc, 4)
+    for x in ("dq", "e_dq"):  # d/dq of f(q / 2)
+        ref[x] = ref[x] * 0.5
+    ref["r_dq"] = ref["r_dq"] * 0.25
+    check_all("scale", dict(out=out, lse=lse, dq=dq, dk=dk, dv=dv), ref)
+
+
+def test_ids_in_any_order():
+    """Document ids that fall from one document to the next, and every id negative or repeated refused."""
+    c = make_case(W(2, 2, 1, 64, 700, 2, ("uniform", 60, 300, 30), 50), 1, seed=3)
+    c["doc"] = np.where(c["doc"] > 0, 1000 - c["doc"], 0).astype(np.int32)
+    check_all("falling ids", run(c, 4), reference(c, 4))
+    g = gpu_geom(c)
+    doc = c["doc"].copy()
+    doc[0, :20] = doc[0, 500]  # a local document's id before its run
+    _, status = bdattn.bd_attn_sink_seg_build(torch.from_numpy(doc).cuda(), g, 4)
+    assert int(status.item()) == bdattn.STATUS_LAYOUT
