@@ -109,11 +109,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* vstatus = status;
 
   const int item = blockIdx.x / g.Hkv;
+  // thread 0 reads the counts and, in the same trip, its item of the work list
+  // (the units' only once the table is known to have them)
+  int work_item = 0, before = 0;
+  int4 u0 = make_int4(0, 0, 0, 0), u1 = u0;  // kSink: the unit
   if (tid == 0) {
     // the attended K/V tiles lead the work list; the grid must cover them
+    before = *vstatus;
+    if (!kSink && item < g.B * g.nkt) work_item = seg[g.off[BD_SEG_OFF_BWD_WORK] + item];
     // (kSink: units, which cover the attended tiles)
     const int n_att = seg[g.off[BD_SEG_OFF_COUNTS] + 3];
     const int n_work = kSink ? sink_n_units(g, seg) : n_att;
+    if (kSink && item < n_work) {
+      const int4* u =
+          reinterpret_cast<const int4*>(seg + g.sk_off + kSinkHdrWords + static_cast<size_t>(item) * kSinkUnitWords);
+      u0 = u[0];
+      u1 = u[1];
+    }
     int mode = kModeIdle;
     s.n_att = -1;
     if (n_att < 0 || n_att > g.B * g.nkt || n_work < n_att || n_work > static_cast<int>(gridDim.x) / g.Hkv) {
@@ -140,32 +152,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (tid == 0) {
-    const int32_t* u = kSink ? seg + g.sk_off + kSinkHdrWords + static_cast<size_t>(item) * kSinkUnitWords : nullptr;
-    const int wi = kSink ? u[0] : seg[g.off[BD_SEG_OFF_BWD_WORK] + item];
+    const int wi = kSink ? u0.x : work_item;
     int ok = wi >= 0 && wi < g.B * g.nkt;
     const int b = ok ? wi / g.nkt : 0, kt = ok ? wi % g.nkt : 0;
     const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
-    ok = ok && hdr[kHdrMagic] == kSegMagic && hdr[kHdrRowOffset] == g.row_offset && hdr[kHdrL] == g.L &&
-         hdr[kHdrKvOffset] == g.kv_offset && hdr[kHdrSkv] == g.S_kv && hdr[kHdrWindow] == g.window &&
-         hdr[kHdrSfull] == g.S_full && hdr[kHdrSink] == g.n_sink;
+    const bool hdr_ok = seg_hdr_ok(g, hdr);
     const int n_real = hdr[BD_SEG_N_REAL];
-    const int32_t* qr = seg + g.off[BD_SEG_OFF_KT_QRANGE] + (b * g.nkt + kt) * 2;
-    const int qlo = kSink ? u[1] : qr[0], qhi = kSink ? u[2] : qr[1];
+    const int2 qr = kSink ? make_int2(u0.y, u0.z)
+                          : *reinterpret_cast<const int2*>(seg + g.off[BD_SEG_OFF_KT_QRANGE] + (b * g.nkt + kt) * 2);
+    const int qlo = qr.x, qhi = qr.y;
     if constexpr (kSink) {
-      s.u_primary = u[3];
-      s.u_slot = u[4];
-      s.u_rbase = u[5];
-      ok = ok && u[4] < g.sk_slots && u[5] >= 0 && u[5] < kTile;
+      s.u_primary = u0.w;
+      s.u_slot = u1.x;
+      s.u_rbase = u1.y;
+      ok = ok && u1.x < g.sk_slots && u1.y >= 0 && u1.y < kTile;
     }
     // an attended tile has a non-empty q range
-    ok = ok && n_real >= 0 && n_real <= g.L && qlo >= 0 && qhi <= n_real && qlo < qhi;
+    ok = ok && hdr_ok && n_real >= 0 && n_real <= g.L && qlo >= 0 && qhi <= n_real && qlo < qhi;
     if (!ok) atomicOr(status, BD_STATUS_BOUNDS);
     s.b = b;
     s.kt = kt;
     s.q_lo = qlo / kQ;
     s.nq = qhi > qlo ? (qhi - 1) / kQ - qlo / kQ + 1 : 0;
     s.n_real = n_real;
-    s.skip = (!ok || *vstatus != 0) ? 1 : 0;
+    s.skip = (!ok || before != 0) ? 1 : 0;
     s.abort_flag = 0;
     mbar_init(&s.kv_full, 1);
     for (int i = 0; i < 2; ++i) {

@@ -55,6 +55,24 @@ __host__ __device__ inline void seg_layout(int B, int L, int S_kv, int* off, int
   off[BD_SEG_OFF_TOTAL] = o;
 }
 
+// Header words that record the geometry the table was built for.
+constexpr int kHdrRowOffset = 16, kHdrL = 17, kHdrKvOffset = 18, kHdrSkv = 19, kHdrWindow = 20,
+              kHdrSfull = 21, kHdrMagic = 22,
+              kHdrKvChunk = 23,  // 1: table built for one K/V chunk (no K/V range requirement)
+              kHdrSink = 24,     // n_sink the table was built for (0 in ordinary tables)
+              kHdrSinkTab = 25;  // 1: the sink regions follow the table
+constexpr int kSegMagic = 0x62646174;  // "bdat"
+
+// Whether a batch row's header was written for this geometry: three 16-byte
+// loads and no branch between them (each a trip to L2 that a CTA starts with).
+__device__ __forceinline__ bool seg_hdr_ok(const Geom& g, const int32_t* hdr) {
+  const int4 a = *reinterpret_cast<const int4*>(hdr + kHdrRowOffset);
+  const int4 c = *reinterpret_cast<const int4*>(hdr + kHdrWindow);
+  const int4 e = *reinterpret_cast<const int4*>(hdr + kHdrSink);
+  return (a.x == g.row_offset) & (a.y == g.L) & (a.z == g.kv_offset) & (a.w == g.S_kv) & (c.x == g.window) &
+         (c.y == g.S_full) & (c.z == kSegMagic) & (e.x == g.n_sink) & (e.y == g.sink_tab || g.sink_tab == 0);
+}
+
 // ---- sink tables -----------------------------------------------------------
 // A sink's gradient sums over all later rows of its document: with a window W,
 // the rows that attend a K/V tile are a short range, except that a tile that
@@ -94,14 +112,6 @@ __host__ __device__ inline long long plan_layout(int B, int W, int L, int* off) 
   off[BD_PLAN_OFF_TOTAL] = static_cast<int>(o);
   return o;
 }
-
-// Header words that record the geometry the table was built for.
-constexpr int kHdrRowOffset = 16, kHdrL = 17, kHdrKvOffset = 18, kHdrSkv = 19, kHdrWindow = 20,
-              kHdrSfull = 21, kHdrMagic = 22,
-              kHdrKvChunk = 23,  // 1: table built for one K/V chunk (no K/V range requirement)
-              kHdrSink = 24,     // n_sink the table was built for (0 in ordinary tables)
-              kHdrSinkTab = 25;  // 1: the sink regions follow the table
-constexpr int kSegMagic = 0x62646174;  // "bdat"
 
 // The allowed key interval [lo, hi] (global positions) of a real local row i:
 // hi = p, lo = max(doc_start, p - W + 1).
@@ -152,15 +162,14 @@ __host__ __device__ inline long long sink_words(const Geom& g) {
 // documents that start inside it: RowKeys); a tile may come up in both walks.
 // Where a sink
 // tile's sinks fit 32 columns from a 16-column boundary on, col[] is the first of
-// them and the pass works on 32 keys instead of 128, else -1.
-__device__ inline void sink_passes(const Geom& g, const int32_t* seg, int b, int qt, int n_real, int* x0, int* nx,
-                                   int* col) {
+// them and the pass works on 32 keys instead of 128, else -1. ds: the document
+// start of the q tile's first row (row_lo).
+__device__ inline void sink_passes(const Geom& g, int ds, int qt, int n_real, int* x0, int* nx, int* col) {
   *x0 = *nx = 0;
   col[0] = col[1] = -1;
   const int first = qt * kTile;
   if (g.window <= 0 || g.n_sink <= 0 || first >= n_real) return;
   const int last = first + kTile - 1 < n_real - 1 ? first + kTile - 1 : n_real - 1;
-  const int ds = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + first];
   const int lo = g.row_offset + last - g.window + 1;  // no row of the document sees a window key before it
   if (ds < 0 || lo <= ds) return;
   const int a = ds > g.kv_offset ? ds - g.kv_offset : 0;
@@ -204,13 +213,11 @@ __device__ __forceinline__ uint32_t keep_bits32(const uint32_t (&km)[4], int c0)
   return (c0 & 16) ? (lo >> 16) | (hi << 16) : lo;
 }
 
-// Units of a sink table, or -1 when the table is not one for this geometry.
+// Units of a sink table, or -1 when the table is not one for this geometry
+// (the regions' places follow from it).
 __device__ __forceinline__ int sink_n_units(const Geom& g, const int32_t* seg) {
   const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR];
-  if (hdr[kHdrMagic] != kSegMagic || hdr[kHdrSink] != g.n_sink || hdr[kHdrSinkTab] != 1 || hdr[kHdrL] != g.L ||
-      hdr[kHdrSkv] != g.S_kv || hdr[kHdrWindow] != g.window || hdr[kHdrRowOffset] != g.row_offset ||
-      hdr[kHdrKvOffset] != g.kv_offset)
-    return -1;  // the capacities, and so the regions' places, follow from these
+  if (!seg_hdr_ok(g, hdr) || hdr[kHdrSinkTab] != 1) return -1;
   const int n = seg[g.sk_off];
   return n <= g.sk_units ? n : -1;
 }

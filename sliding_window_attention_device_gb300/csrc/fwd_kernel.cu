@@ -84,25 +84,25 @@ __global__ void __launch_bounds__(128 + NQ * 128, 1)
 
   if (tid == 0) {
     const int item = blockIdx.x / n_pairs;
+    const int before = *vstatus;
     const int wi = seg[g.off[BD_SEG_OFF_FWD_WORK] + item];
     int ok = wi >= 0 && wi < g.B * g.nqt;
     const int b = ok ? wi / g.nqt : 0, qt = ok ? wi % g.nqt : 0;
     const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS;
-    ok = ok && hdr[kHdrMagic] == kSegMagic && hdr[kHdrRowOffset] == g.row_offset && hdr[kHdrL] == g.L &&
-         hdr[kHdrKvOffset] == g.kv_offset && hdr[kHdrSkv] == g.S_kv && hdr[kHdrWindow] == g.window &&
-         hdr[kHdrSfull] == g.S_full && hdr[kHdrSink] == g.n_sink;
+    const bool hdr_ok = seg_hdr_ok(g, hdr);
     const int n_real = hdr[BD_SEG_N_REAL];
-    const int32_t* kr = seg + g.off[BD_SEG_OFF_QT_KRANGE] + (b * g.nqt + qt) * 2;
-    const int kt_lo = kr[0], kt_hi = kr[1];
+    const int2 kr = *reinterpret_cast<const int2*>(seg + g.off[BD_SEG_OFF_QT_KRANGE] + (b * g.nqt + qt) * 2);
+    const int first_doc = kSink ? seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + qt * kTile] : 0;
+    const int kt_lo = kr.x, kt_hi = kr.y;
     int nk = kt_hi >= kt_lo ? kt_hi - kt_lo + 1 : 0;
-    ok = ok && n_real >= 0 && n_real <= g.L && (nk == 0 || (kt_lo >= 0 && kt_hi < g.nkt));
+    ok = ok && hdr_ok && n_real >= 0 && n_real <= g.L && (nk == 0 || (kt_lo >= 0 && kt_hi < g.nkt));
     if (!ok) atomicOr(status, BD_STATUS_BOUNDS);
     s.b = b;
     s.qt = qt;
     if constexpr (kSink) {
       // nk counts the sink passes too: pass j is tile x0 + j below nx, kt_lo + j - nx above
       s.x0 = s.nx = 0;
-      if (ok) sink_passes(g, seg, b, qt, n_real, &s.x0, &s.nx, s.col);
+      if (ok) sink_passes(g, first_doc, qt, n_real, &s.x0, &s.nx, s.col);
       nk += s.nx;
       s.kt_lo = kt_lo - s.nx;
     } else {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(128 + NQ * 128, 1)
     }
     s.nk = nk;
     s.n_real = n_real;
-    s.skip = (!ok || *vstatus != 0) ? 1 : 0;
+    s.skip = (!ok || before != 0) ? 1 : 0;
     s.abort_flag = 0;
     for (int i = 0; i < NS; ++i) {
       mbar_init(&s.k_full[i], 1);

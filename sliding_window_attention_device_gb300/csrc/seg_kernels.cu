@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(1024) classify_kernel(Geom g, int32_t* __restr
       if (g.n_sink > 0) {
         const int b = item / g.nqt;
         int x0, nx, col[2];
-        sink_passes(g, seg, b, item % g.nqt, seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL], &x0,
-                    &nx, col);
+        sink_passes(g, seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + item % g.nqt * kTile], item % g.nqt,
+                    seg[g.off[BD_SEG_OFF_HDR] + b * BD_SEG_HDR_WORDS + BD_SEG_N_REAL], &x0, &nx, col);
         key += nx;
       }
       return key;
