@@ -73,6 +73,9 @@ __device__ __forceinline__ bool seg_hdr_ok(const Geom& g, const int32_t* hdr) {
          (c.y == g.S_full) & (c.z == kSegMagic) & (e.x == g.n_sink) & (e.y == g.sink_tab || g.sink_tab == 0);
 }
 
+// The kernels' kSink: ordinary, with sinks, with sinks and a window below kTile.
+constexpr int kNoSink = 0, kSinkLong = 1, kSinkShort = 2;
+
 // ---- sink tables -----------------------------------------------------------
 // A sink's gradient sums over all later rows of its document: with a window W,
 // the rows that attend a K/V tile are a short range, except that a tile that
@@ -194,6 +197,7 @@ struct RowKeys {
   int slo = 1, shi = 0;
   bool inner = false;
 };
+template <int kSink>
 __device__ __forceinline__ RowKeys row_sinks(const Geom& g, int doc_start, int jlo, int p0) {
   RowKeys k;
   const int d = doc_start - g.kv_offset;
@@ -201,7 +205,7 @@ __device__ __forceinline__ RowKeys row_sinks(const Geom& g, int doc_start, int j
   k.slo = d;
   k.shi = (d + g.n_sink < jlo ? d + g.n_sink : jlo) - 1;
   if (k.shi > g.S_kv - 1) k.shi = g.S_kv - 1;  // a K/V chunk may end among them
-  k.inner = doc_start > p0;
+  if constexpr (kSink == kSinkShort) k.inner = doc_start > p0;
   return k;
 }
 

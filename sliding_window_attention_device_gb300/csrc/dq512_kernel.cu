@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads5, 1)
       const int doc_start = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + i];
       jlo = row_lo_window(doc_start, p, g.window) - g.kv_offset;
       jhi = min(p - g.kv_offset, g.S_kv - 1);  // a K/V chunk may end before the row
-      if constexpr (kSink) sk = row_sinks(g, doc_start, jlo, g.row_offset + qt * kTile);
+      if constexpr (kSink) sk = row_sinks<kSinkShort>(g, doc_start, jlo, g.row_offset + qt * kTile);
       nl2 = lse[row0 + i] * -1.4426950408889634f;
       ndl = delta[row0 + i] * -g.scale;  // dS is formed pre-scaled: scale * P (dP - delta)
     }

@@ -24,6 +24,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "dropout.cuh"
 #include "pipeline.cuh"
@@ -57,7 +58,7 @@ static_assert(2 * 2 * kChunkB256 >= kTile * kD256 * 2, "out staging fits ring sl
 
 // kMerge: merge this K/V chunk's result into the running (out, lse) instead
 // of writing it (log-sum-exp weights, as the merge kernel).
-template <bool kMerge, bool kDrop, bool kSink>
+template <bool kMerge, bool kDrop, int kSink>
 __global__ void __launch_bounds__(kThreadsF256, 1)
     fwd256_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const int32_t* __restrict__ seg, const Geom g,
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
       const int doc_start = seg[g.off[BD_SEG_OFF_ROW_LO] + b * g.L + i];
       jlo = row_lo_window(doc_start, p, g.window) - g.kv_offset;
       jhi = min(p - g.kv_offset, g.S_kv - 1);  // a K/V chunk may end before the row
-      if constexpr (kSink) sk = row_sinks(g, doc_start, jlo, g.row_offset + qt * kTile);
+      if constexpr (kSink) sk = row_sinks<kSink>(g, doc_start, jlo, g.row_offset + qt * kTile);
     }
     const float sl2 = g.scale * 1.4426950408889634f;
     float m = -INFINITY, l = 0.f;
@@ -390,11 +391,11 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
         if (t < nx) {
           wlo = sk.inner ? 1 : sk.slo;
           whi = sk.inner ? 0 : sk.shi;
-        } else {
+        } else if (kSink == kSinkShort) {
           inner = sk.inner && sk.shi >= c0 && sk.slo <= c0 + kTile - 1;
         }
       }
-      const bool any_inner = kSink && __any_sync(0xffffffffu, inner);
+      const bool any_inner = kSink == kSinkShort && __any_sync(0xffffffffu, inner);
       const bool dead = !inner && (whi < c0 || wlo > c0 + kTile - 1);
       const bool unmasked = __all_sync(0xffffffffu, dead || (wlo <= c0 && c0 + kTile - 1 <= whi));
       const int a_lo = wlo - c0, e_hi = whi - c0;
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreadsF256, 1)
         if (unmasked) {
 #pragma unroll
           for (int c = 64 * hf; c < 64 * hf + 64; ++c) x[c] = __uint_as_float(xr[c]);
-        } else if (kSink && any_inner) {
+        } else if (kSink == kSinkShort && any_inner) {
           const int b_lo = inner ? sk.slo - c0 : 1, b_hi = inner ? sk.shi - c0 : 0;
 #pragma unroll
           for (int c = 64 * hf; c < 64 * hf + 64; ++c)
@@ -572,10 +573,14 @@ cudaError_t launch_fwd256(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   e = cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e != cudaSuccess) return e;
   if (smem > static_cast<size_t>(max_optin)) return cudaErrorInvalidValue;
-  auto kern = g.n_sink ? (g.drop_t ? (merge ? fwd256_kernel<true, true, true> : fwd256_kernel<false, true, true>)
-                                   : (merge ? fwd256_kernel<true, false, true> : fwd256_kernel<false, false, true>))
-                       : (g.drop_t ? (merge ? fwd256_kernel<true, true, false> : fwd256_kernel<false, true, false>)
-                                   : (merge ? fwd256_kernel<true, false, false> : fwd256_kernel<false, false, false>));
+  auto pick = [&](auto sink) {
+    constexpr int kS = decltype(sink)::value;
+    return g.drop_t ? (merge ? fwd256_kernel<true, true, kS> : fwd256_kernel<false, true, kS>)
+                    : (merge ? fwd256_kernel<true, false, kS> : fwd256_kernel<false, false, kS>);
+  };
+  auto kern = !g.n_sink            ? pick(std::integral_constant<int, kNoSink>())
+              : g.window >= kTile ? pick(std::integral_constant<int, kSinkLong>())
+                                  : pick(std::integral_constant<int, kSinkShort>());
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(g.B) * g.nqt * g.Hq;  // (q tile, query head)
