@@ -60,6 +60,7 @@ struct Ctl {
   int abort_flag;
   int b, kt, q_lo, nq, n_real, skip, mode, n_att;
   int u_primary, u_slot, u_rbase;  // kSink: the unit's kind, partial slot and first partial row
+  int u_head0, u_heads;            // and its heads of the group
 };
 
 // What a CTA does, from its position in the backward work list.
@@ -165,7 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.u_primary = u0.w;
       s.u_slot = u1.x;
       s.u_rbase = u1.y;
-      ok = ok && u1.x < g.sk_slots && u1.y >= 0 && u1.y < kTile;
+      s.u_head0 = u1.z;
+      s.u_heads = u1.w;
+      ok = ok && u1.x < g.sk_slots && u1.y >= 0 && u1.y < kTile && u1.z >= 0 && u1.w > 0 && u1.z + u1.w <= g.G;
     }
     // an attended tile has a non-empty q range
     ok = ok && hdr_ok && n_real >= 0 && n_real <= g.L && qlo >= 0 && qhi <= n_real && qlo < qhi;
@@ -197,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (s.skip) return;
   const int b = s.b, kt = s.kt, q_lo = s.q_lo, nq = s.nq, n_real = s.n_real;
-  const int G = g.G;
+  const int G = kSink ? s.u_heads : g.G;                       // query heads of this CTA's work
+  const int h_first = hk * g.G + (kSink ? s.u_head0 : 0);
   const int n_it = G * nq;  // iteration it: query head hk*G + it / nq, q tile q_lo + it % nq
   // dK / dV row j of this (batch row, kv head): kv_row(g, b, hk, j)
   const bool is_pds = (warp >= 4 && warp < 8) || warp >= 12;
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int issued = 0, gq = 0, qt = 0;  // (head, q tile) of iteration `it`
     for (int it = 0; it < n_it; ++it) {
       const int st = it & 1;
-      const int h = hk * G + gq, q0 = (q_lo + qt) * kQ;
+      const int h = h_first + gq, q0 = (q_lo + qt) * kQ;
       // fetch this tile's per-row values before waiting for the free stage
       float l2[4], dl[4];
 #pragma unroll
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q0 = (q_lo + qt) * kQ;
       uint64_t km = 0;  // dropout: keep bits of this key over the half's 64 q columns
       if constexpr (kDrop)
-        km = key_keep_mask<8>(g, b, hk * G + gq, g.row_offset + q0 + c0, g.kv_offset + kt * kTile + (warp & 3) * 32,
+        km = key_keep_mask<8>(g, b, h_first + gq, g.row_offset + q0 + c0, g.kv_offset + kt * kTile + (warp & 3) * 32,
                               lane);
       if (++qt == nq) {
         qt = 0;
@@ -553,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int gq = 0, qt = 0;
     for (int it = 0; it < n_it; ++it) {
-      const int h = hk * G + gq, q0 = (q_lo + qt) * kQ;
+      const int h = h_first + gq, q0 = (q_lo + qt) * kQ;
       if (++qt == nq) {
         qt = 0;
         ++gq;

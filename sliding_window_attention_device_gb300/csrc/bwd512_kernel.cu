@@ -72,6 +72,7 @@ struct Bwd512Smem {
   int abort_flag;
   int b, kt, q64_lo, nq64, n_real, skip, work, n_att;
   int u_primary, u_slot, u_rbase;  // kSink: the unit's kind, partial slot and first partial row
+  int u_head0, u_heads;            // and its heads of the group
 };
 
 __device__ __forceinline__ void red_add_f32(float* addr, float v) {
@@ -155,7 +156,9 @@ __global__ void __launch_bounds__(kThreads5, 1)
       s.u_primary = u0.w;
       s.u_slot = u1.x;
       s.u_rbase = u1.y;
-      ok = ok && u1.x < g.sk_slots && u1.y >= 0 && u1.y < kTile;
+      s.u_head0 = u1.z;
+      s.u_heads = u1.w;
+      ok = ok && u1.x < g.sk_slots && u1.y >= 0 && u1.y < kTile && u1.z >= 0 && u1.w > 0 && u1.z + u1.w <= g.G;
     }
     // an attended tile has a non-empty q range
     ok = ok && hdr_ok && n_real >= 0 && n_real <= g.L && qlo >= 0 && qhi <= n_real && qlo < qhi;
@@ -190,7 +193,8 @@ __global__ void __launch_bounds__(kThreads5, 1)
   __syncthreads();
   if (s.skip) return;
   const int b = s.b, kt = s.kt, q64_lo = s.q64_lo, nq64 = s.nq64, n_real = s.n_real;
-  const int G = g.G;
+  const int G = kSink ? s.u_heads : g.G;                       // query heads of this CTA's work
+  const int h_first = hk * g.G + (kSink ? s.u_head0 : 0);
   const int n_it = G * nq64;  // (query head of the group, 64-row q tile) steps
   // P / dS warpgroups: warps 4-7 (half 0, q columns 0-31) and 12-15 (half 1, 32-63)
   const bool is_pds = (warp >= 4 && warp < 8) || warp >= 12;
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(kThreads5, 1)
 
   auto decode = [&](int it, int& h, int& q0) {
     const int gq = it / nq64;
-    h = hk * G + gq;
+    h = h_first + gq;
     q0 = (q64_lo + it - gq * nq64) * kBwdQ;
   };
 

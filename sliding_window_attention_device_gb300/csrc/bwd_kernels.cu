@@ -161,6 +161,7 @@ struct BwdSmem {
   int abort_flag;
   int b, kt, q64_lo, nq64, n_real, skip, mode, n_att;
   int u_primary, u_slot, u_rbase;  // kSink: the unit's kind, partial slot and first partial row
+  int u_head0, u_heads;            // and its heads of the group
 };
 
 constexpr int kBwdThreads = 512;
@@ -248,7 +249,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       s.u_primary = u0.w;
       s.u_slot = u1.x;
       s.u_rbase = u1.y;
-      ok = ok && u1.x < g.sk_slots && u1.y >= 0 && u1.y < kTile;
+      s.u_head0 = u1.z;
+      s.u_heads = u1.w;
+      ok = ok && u1.x < g.sk_slots && u1.y >= 0 && u1.y < kTile && u1.z >= 0 && u1.w > 0 && u1.z + u1.w <= g.G;
     }
     // an attended tile has a non-empty q range
     ok = ok && hdr_ok && n_real >= 0 && n_real <= g.L && qlo >= 0 && qhi <= n_real && qlo < qhi;
@@ -283,7 +286,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   if (s.skip) return;
   const int b = s.b, kt = s.kt, q64_lo = s.q64_lo, nq64 = s.nq64, n_real = s.n_real;
-  const int G = g.G;
+  const int G = kSink ? s.u_heads : g.G;                       // query heads of this CTA's work
+  const int h_first = hk * g.G + (kSink ? s.u_head0 : 0);
   const int n_it_pass = G * nq64;
   const int n_it = kPasses * n_it_pass;
   // dK / dV row j of this (batch row, kv head): kv_row(g, b, hk, j)
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     pass = it / n_it_pass;
     const int rem = it - pass * n_it_pass;
     const int gq = rem / nq64;
-    h = hk * G + gq;
+    h = h_first + gq;
     q0 = (q64_lo + rem - gq * nq64) * kBwdQ;
   };
 

@@ -8,6 +8,7 @@
 namespace bd {
 
 constexpr int kTile = 128;          // q rows / K-V rows per tile (forward, classification)
+constexpr int kSms = 152;           // SMs of a GB300
 constexpr int kBwdQ = 64;           // q rows per backward iteration
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // pipeline wait limit (2 s)
 constexpr int kAbortBits = BD_STATUS_TIMEOUT;      // other CTAs' errors that end a wait early
@@ -30,6 +31,8 @@ struct Geom {
   int sk_units, sk_sums, sk_slots;  // capacities of the unit list, the sum list and the partial slots
   int sk_rows;                    // key rows of a partial slot
   int sk_split;                   // 128-row q tiles of a unit
+  int sk_heads;                   // query heads of a unit (G, unless the work is cut finely)
+  int sk_fine;                    // 1: few tiles, so units are cut by q rows and heads alike
   float* sk_part;                 // partial slots of a backward, in the caller's workspace
 };
 
@@ -87,8 +90,13 @@ constexpr int kNoSink = 0, kSinkLong = 1, kSinkShort = 2;
 // directly; the units of a tile with several write those sinks' key rows,
 // [rbase, rbase + sk_rows), as fp32 partials into slots of the workspace, which
 // a last kernel adds in slot order, and the primary writes the other rows.
+// Where the tiles are too few to occupy the SMs (sk_fine), every tile's rows are
+// cut into units of sk_split q tiles and sk_heads query heads of the group, and
+// all 128 key rows of a tile with several units go through slots: one head dim
+// 256 unit of 8 heads and 8 q tiles is 0.4 ms of products in sequence.
 constexpr int kSinkHdrWords = 8;   // n_units, n_sums, n_slots
-constexpr int kSinkUnitWords = 8;  // item (b * nkt + kt), q_begin, q_end (local rows), primary, slot (-1: none), rbase
+constexpr int kSinkUnitWords = 8;  // item (b * nkt + kt), q_begin, q_end (local rows), primary, slot (-1:
+                                   // none), rbase, first head of the group, heads
 constexpr int kSinkSumWords = 4;   // item, first slot, slots, rbase
 
 // Row index of (batch row b, kv head hk, K/V buffer row j) in k, v, dk, dv.
@@ -125,26 +133,51 @@ __device__ __forceinline__ int row_lo_window(int doc_start, int p, int window) {
 // Capacities of a sink table and its partial slots. A tile has several units
 // only if its last document has more than (sk_split - 2) * kTile local rows, so
 // at most L / that many documents count, each with its sinks (n <= 128) in at
-// most two tiles; a document's rows are cut once for each of the two.
+// most two tiles; a document's rows are cut once for each of the two. Cut
+// finely, any tile may have several: its window's q tiles and its sinks' tails.
 __host__ __device__ inline void sink_sizes(Geom* g) {
   const bool on = g->window > 0 && g->n_sink > 0;
   g->sk_rows = g->n_sink > 0 ? g->n_sink : 1;
-  const int w_tiles = g->window / kTile + 1;
+  g->sk_heads = g->G;
+  g->sk_fine = 0;
+  const int w_tiles = g->window > 0 ? g->window / kTile + 1 : g->nqt;
   g->sk_split = w_tiles > 8 ? w_tiles : 8;  // a unit about as long as a window's, and not short
-  long long t = 0, e = 0;
-  if (on) {
-    t = 2LL * (g->L / ((g->sk_split - 2) * kTile) + 1);
-    if (t > g->nkt) t = g->nkt;
-    e = t + 2LL * (g->L / (g->sk_split * kTile)) + 2;
-  }
   // tiles with a unit: those reachable by position through the window, and the
   // straddling document's sinks
   const long long hi = static_cast<long long>(g->row_offset) + g->L - 1 - g->kv_offset;
   const long long lo = g->window > 0 ? static_cast<long long>(g->row_offset) - g->window + 1 - g->kv_offset : 0;
   const long long a = lo > 0 ? lo : 0;
   const long long z = hi < g->S_kv - 1 ? hi : static_cast<long long>(g->S_kv) - 1;
-  long long reach = (z < a ? 0 : z / kTile - a / kTile + 1) + (on ? 2 : 0);
+  const long long seen = z < a ? 0 : z / kTile - a / kTile + 1;
+  long long reach = seen + (on ? 2 : 0);
   if (reach > g->nkt) reach = g->nkt;
+  // Half the SMs or fewer with a tile, and four or more (head, q tile) steps in
+  // the longest unit: cut to an SM's share of all the steps, by heads first.
+  const int slices = g->D == 512 ? 4 : 1;
+  const long long ctas = g->B * (seen > 0 ? seen : 1) * g->Hkv * slices;
+  const int longest = g->nqt < g->sk_split ? g->nqt : g->sk_split;  // q tiles
+  if (on && 2 * ctas <= kSms && static_cast<long long>(g->G) * longest >= 4) {
+    const int near = w_tiles + 1 < g->nqt ? w_tiles + 1 : g->nqt;
+    const long long steps = static_cast<long long>(g->B) * g->Hkv * slices * g->G * (seen * near + g->nqt);
+    const long long share = steps / kSms > 1 ? steps / kSms : 1;
+    const int by = share < g->G ? static_cast<int>((g->G + share - 1) / share) : 1;  // groups of heads
+    g->sk_fine = 1;
+    g->sk_rows = kTile;
+    g->sk_heads = cdiv(g->G, by);
+    const long long split = share / g->sk_heads;
+    g->sk_split = split < 1 ? 1 : split < longest ? static_cast<int>(split) : longest;
+  }
+  const int hs = cdiv(g->G, g->sk_heads);
+  long long t = 0, e = 0;  // tiles with several units; units beyond the first of a tile
+  if (g->sk_fine) {
+    const long long win = w_tiles + 2 < g->nqt ? w_tiles + 2 : g->nqt;
+    t = reach;
+    e = hs * (reach + (reach * (win + 2) + 2LL * g->nqt) / g->sk_split + 2);
+  } else if (on) {
+    t = 2LL * (g->L / ((g->sk_split - 2) * kTile) + 1);
+    if (t > g->nkt) t = g->nkt;
+    e = t + 2LL * (g->L / (g->sk_split * kTile)) + 2;
+  }
   g->sk_sums = static_cast<int>(g->B * t);
   g->sk_slots = static_cast<int>(g->B * (t + e));
   g->sk_units = static_cast<int>(g->B * (reach + e));

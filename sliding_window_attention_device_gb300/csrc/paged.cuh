@@ -30,8 +30,7 @@ __device__ __forceinline__ uint32_t page_row(const PagedGeom& g, int page, int h
 // Decode: CTAs, warps per CTA, keys per warp step and query heads per CTA.
 constexpr int kDecWarps = 4;
 constexpr int kDecKeys = 16;
-constexpr int kDecSms = 152;
-__host__ __device__ inline int dec_ctas(int D) { return D <= 256 ? 2 * kDecSms : kDecSms; }
+__host__ __device__ inline int dec_ctas(int D) { return D <= 256 ? 2 * kSms : kSms; }
 __host__ __device__ inline int dec_head_tiles(int D, int G) { return D <= 256 && G > 8 ? 2 : 1; }
 // Whether a CTA takes whole rows: no sequence can show a new token many keys,
 // or not very many and there are rows for most SMs.

@@ -81,7 +81,7 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int3
                                 void* v_pages, int32_t* status, cudaStream_t st) {
   if (n_tokens == 0) return cudaSuccess;
   // a token per CTA until the CTAs fill the machine four times over
-  int tok = (n_tokens + 4 * kDecSms - 1) / (4 * kDecSms);
+  int tok = (n_tokens + 4 * kSms - 1) / (4 * kSms);
   tok = tok < 1 ? 1 : tok > kAppendTok ? kAppendTok : tok;
   const unsigned grid = static_cast<unsigned>((n_tokens + tok - 1) / tok);
   if (const cudaError_t le =

@@ -307,8 +307,9 @@ __device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int n
   int32_t* units = hdr + kSinkHdrWords;
   int32_t* sums = units + static_cast<size_t>(g.sk_units) * kSinkUnitWords;
   const int n_items = g.B * g.nkt, span = g.sk_split * kTile;
-  auto bin_of = [&](int beg, int end) { return nbins - 1 - min((end - 1) / kBwdQ - beg / kBwdQ + 1, nbins - 1); };
-  // units of a tile: rows [beg, end0), then pieces of `span` up to end; returns their number
+  const int hs = cdiv(g.G, g.sk_heads);
+  // units of a tile: rows [beg, end0), then pieces of `span` up to end, each for every
+  // group of sk_heads heads; returns their number
   auto ranges = [&](int item, int* beg, int* end0, int* end, int* rbase) -> int {
     const int b = item / g.nkt, kt = item % g.nkt;
     int wb, we, sb, se;
@@ -323,8 +324,19 @@ __device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int n
     *beg = wb;
     *end = max(we, se);
     if (*beg >= *end) return 0;
-    *end0 = min(*end, max((wb / kTile) * kTile + span, cdiv(we, kTile) * kTile));
-    return 1 + cdiv(*end - *end0, span);
+    const int first = (wb / kTile) * kTile + span;
+    if (g.sk_fine) *rbase = 0;
+    *end0 = min(*end, g.sk_fine ? first : max(first, cdiv(we, kTile) * kTile));
+    return (1 + cdiv(*end - *end0, span)) * hs;
+  };
+  // unit x of the tile: rows [*ub, *ue), the group's heads [*h0, *h0 + *nh); returns its bin
+  auto unit_of = [&](int x, int beg, int end0, int end, int* ub, int* ue, int* h0, int* nh) -> int {
+    const int y = x / hs;
+    *ub = y == 0 ? beg : end0 + (y - 1) * span;
+    *ue = y == 0 ? end0 : min(end, end0 + y * span);
+    *h0 = (x % hs) * g.sk_heads;
+    *nh = min(g.sk_heads, g.G - *h0);
+    return nbins - 1 - min((*ue - 1) / kBwdQ - *ub / kBwdQ + 1, nbins - 1);
   };
   for (int x = tid; x < nbins; x += nthr) s_hist[x] = 0;
   __syncthreads();
@@ -332,8 +344,10 @@ __device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int n
   for (int item = tid; item < n_items; item += nthr) {
     int beg, end0, end, rbase;
     const int n = ranges(item, &beg, &end0, &end, &rbase);
-    for (int x = 0; x < n; ++x)
-      atomicAdd(&s_hist[x == 0 ? bin_of(beg, end0) : bin_of(end0 + (x - 1) * span, min(end, end0 + x * span))], 1);
+    for (int x = 0; x < n; ++x) {
+      int ub, ue, h0, nh;
+      atomicAdd(&s_hist[unit_of(x, beg, end0, end, &ub, &ue, &h0, &nh)], 1);
+    }
     n_units += n;
   }
   n_units = block_add(n_units, s_red);
@@ -367,8 +381,8 @@ __device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int n
       e[3] = rbase;
     }
     for (int x = 0; x < n; ++x) {
-      const int ub = x == 0 ? beg : end0 + (x - 1) * span, ue = x == 0 ? end0 : min(end, end0 + x * span);
-      const int pos = atomicAdd(&s_hist[bin_of(ub, ue)], 1);
+      int ub, ue, h0, nh;
+      const int pos = atomicAdd(&s_hist[unit_of(x, beg, end0, end, &ub, &ue, &h0, &nh)], 1);
       if (pos >= g.sk_units) continue;
       int32_t* u = units + static_cast<size_t>(pos) * kSinkUnitWords;
       u[0] = item;
@@ -377,7 +391,8 @@ __device__ void build_sink_units(const Geom& g, int32_t* __restrict__ seg, int n
       u[3] = x == 0;
       u[4] = multi ? slot0 + x : -1;
       u[5] = rbase;
-      u[6] = u[7] = 0;
+      u[6] = h0;
+      u[7] = nh;
     }
     n_sums += tot_sums;
     n_slots += tot_slots;

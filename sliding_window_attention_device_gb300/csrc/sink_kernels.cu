@@ -15,7 +15,9 @@
 
 namespace bd {
 
-__global__ void __launch_bounds__(256) sink_sum_kernel(const int32_t* __restrict__ seg, const Geom g,
+constexpr int kSumThreads = 256;
+
+__global__ void __launch_bounds__(kSumThreads) sink_sum_kernel(const int32_t* __restrict__ seg, const Geom g,
                                                        void* __restrict__ dk, void* __restrict__ dv, int grads_bf16,
                                                        const int32_t* status) {
   pdl_begin();
@@ -24,42 +26,43 @@ __global__ void __launch_bounds__(256) sink_sum_kernel(const int32_t* __restrict
   const int n_sums = seg[g.sk_off + 1] < g.sk_sums ? seg[g.sk_off + 1] : g.sk_sums;
   const int32_t* sums = seg + g.sk_off + kSinkHdrWords + static_cast<size_t>(g.sk_units) * kSinkUnitWords;
   const int vpr = g.D / 4, per = g.sk_rows * vpr;  // 4-element pieces of a row, of a slot's dk or dv
+  const int cuts = (2 * per + kSumThreads - 1) / kSumThreads;  // CTAs' worth of pieces of a (sum, kv head)
   const size_t slot_step = static_cast<size_t>(g.Hkv) * 2 * per;
-  for (long long x = blockIdx.x; x < static_cast<long long>(n_sums) * g.Hkv; x += gridDim.x) {
-    const int32_t* e = sums + (x / g.Hkv) * kSinkSumWords;
-    const int hk = static_cast<int>(x % g.Hkv), item = e[0], slot0 = e[1], n = e[2], rbase = e[3];
+  for (long long x = blockIdx.x; x < static_cast<long long>(n_sums) * g.Hkv * cuts; x += gridDim.x) {
+    const int y = static_cast<int>(x % cuts) * kSumThreads + threadIdx.x;
+    if (y >= 2 * per) continue;
+    const int32_t* e = sums + (x / cuts / g.Hkv) * kSinkSumWords;
+    const int hk = static_cast<int>(x / cuts % g.Hkv), item = e[0], slot0 = e[1], n = e[2], rbase = e[3];
     if (item < 0 || item >= g.B * g.nkt || slot0 < 0 || n < 0 || slot0 + n > g.sk_slots) continue;
     const int b = item / g.nkt, kt = item % g.nkt;
-    for (int y = threadIdx.x; y < 2 * per; y += blockDim.x) {
-      const int which = y / per, row = y % per / vpr, c4 = y % vpr;
-      const int r = rbase + row, j = kt * kTile + r;
-      if (r >= kTile || j >= g.S_kv) continue;
-      const float4* p = reinterpret_cast<const float4*>(unit_part(g, slot0, hk, which, row)) + c4;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int k = 0; k < n; ++k) {
-        const float4 v = p[k * slot_step];
-        a.x += v.x;
-        a.y += v.y;
-        a.z += v.z;
-        a.w += v.w;
-      }
-      void* out = which ? dv : dk;
-      const size_t at = kv_row(g, b, hk, j) * vpr + c4;
-      if (grads_bf16)
-        static_cast<uint2*>(out)[at] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-      else
-        static_cast<float4*>(out)[at] = a;
+    const int which = y / per, row = y % per / vpr, c4 = y % vpr;
+    const int r = rbase + row, j = kt * kTile + r;
+    if (r >= kTile || j >= g.S_kv) continue;
+    const float4* p = reinterpret_cast<const float4*>(unit_part(g, slot0, hk, which, row)) + c4;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float4 v = p[k * slot_step];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
     }
+    void* out = which ? dv : dk;
+    const size_t at = kv_row(g, b, hk, j) * vpr + c4;
+    if (grads_bf16)
+      static_cast<uint2*>(out)[at] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    else
+      static_cast<float4*>(out)[at] = a;
   }
 }
 
 cudaError_t launch_sink_sum(const int32_t* seg, const Geom& g, void* dk, void* dv, int bf16, int32_t* status,
                             cudaStream_t st) {
-  const long long n = static_cast<long long>(g.sk_sums) * g.Hkv;
-  if (n == 0) return cudaSuccess;  // no window or no sinks: every tile has one unit
-  const unsigned grid = static_cast<unsigned>(n < 152 * 8 ? n : 152 * 8);
-  if (const cudaError_t le = launch_pdl(sink_sum_kernel, dim3(grid), dim3(256), 0, st, seg, g, dk, dv, bf16, status);
+  const long long n = static_cast<long long>(g.sk_sums) * g.Hkv * ((2LL * g.sk_rows * g.D / 4 + kSumThreads - 1) / kSumThreads);
+  if (n == 0) return cudaSuccess;  // every tile has one unit
+  const unsigned grid = static_cast<unsigned>(n < kSms * 8 ? n : kSms * 8);
+  if (const cudaError_t le = launch_pdl(sink_sum_kernel, dim3(grid), dim3(kSumThreads), 0, st, seg, g, dk, dv, bf16, status);
       le != cudaSuccess) return le;
   return cudaGetLastError();
 }
