@@ -549,7 +549,7 @@ def bd_attn_sink_fwd(q, k, v, seg, g: Geom, n_sink: int, status, out=None, lse=N
             return bd_attn_sink_fwd(q, k, v, seg, g, n_sink, status, out, lse, None, _fn)
     rows, kv = (g.B, g.Hq, g.L, g.D), kv_shape(g)
     if out is None:
-        out = torch.empty(rows, dtype=_BF16, device=dev)
+        out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(rows[:3], dtype=_F32, device=dev)
     _want(dev, (q, "q", _BF16, rows), (k, "k", _BF16, kv), (v, "v", _BF16, kv),
@@ -580,11 +580,11 @@ def bd_attn_sink_bwd(dout, q, k, v, out, lse, seg, g: Geom, n_sink: int, status,
     rows, kv = (g.B, g.Hq, g.L, g.D), kv_shape(g)
     n = sink_bwd_workspace_bytes(g, n_sink)
     if dq is None:
-        dq = torch.empty(rows, dtype=grad_dtype, device=dev)
+        dq = torch.empty_like(q, dtype=grad_dtype)
     if dk is None:
-        dk = torch.empty(kv, dtype=grad_dtype, device=dev)
+        dk = torch.empty_like(k, dtype=grad_dtype)
     if dv is None:
-        dv = torch.empty(kv, dtype=grad_dtype, device=dev)
+        dv = torch.empty_like(v, dtype=grad_dtype)
     if workspace is None:
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     _want(dev, (dout, "dout", _BF16, rows), (q, "q", _BF16, rows), (out, "out", _BF16, rows), (k, "k", _BF16, kv),
@@ -678,7 +678,7 @@ def bd_attn_paged_decode(q, k_pages, v_pages, page_table, seq_lens, pg: Paged, s
     rows, cache = (pg.B, pg.Hq, pg.D), (pg.n_pages, pg.Hkv, pg.page_size, pg.D)
     n = paged_decode_workspace_bytes(pg)
     if out is None:
-        out = torch.empty(rows, dtype=_BF16, device=dev)
+        out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(rows[:2], dtype=_F32, device=dev)
     if workspace is None and n > 16:  # 16: the call needs none

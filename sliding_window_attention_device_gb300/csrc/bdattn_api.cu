@@ -45,6 +45,8 @@ cudaError_t launch_needed_gather(const void* x, const int32_t* plan, int B, int 
 cudaError_t launch_needed_scatter_add(const void* gsend, const int32_t* plan, int B, int C, int L, int vshift,
                                       int bf16, void* glocal, int max_rows, int32_t* status, cudaStream_t st);
 int bwd_q_box_rows(int D);
+cudaError_t launch_sink_finalize(const int32_t* seg, const Geom& g, void* dk, void* dv, void* workspace, void* dq,
+                                 int32_t* status, cudaStream_t st);
 cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int32_t* cu_new, const int32_t* seq_lens,
                                 const int32_t* page_table, const PagedGeom& g, int n_tokens, void* k_pages,
                                 void* v_pages, int32_t* status, cudaStream_t st);
@@ -405,7 +407,7 @@ int bwd_prep_impl(const void* dout, const void* out, const bd_geom* gi, void* wo
 
 int bwd_main_impl(const void* dout, const void* q, const void* k, const void* v, const float* lse, const void* seg,
                   const bd_geom* gi, int n_sink, int grad_dtype, void* dk, void* dv, void* workspace, float* dq_f32,
-                  int32_t* status, bd_stream_t stream) {
+                  int32_t* status, bd_stream_t stream, bool sum = true) {
   Geom g;
   if (int rc = n_sink < 0 ? to_geom(gi, &g) : to_geom_sink(gi, n_sink, &g)) return rc;
   if (!dout || !q || !k || !v || !lse || !seg || !dk || !dv || !workspace || !status) return BD_ERR_ARG;
@@ -428,7 +430,7 @@ int bwd_main_impl(const void* dout, const void* q, const void* k, const void* v,
   if (g.sink_tab) set_sink_part(&g, workspace);
   if (int rc = cuda_rc(launch_bwd_main(mq, mdo, mk, mv, mdq, sg, g, lse, dk, dv, bf16, workspace, dq_f32, status, st)))
     return rc;
-  return g.sink_tab ? cuda_rc(launch_sink_sum(sg, g, dk, dv, bf16, status, st)) : BD_OK;
+  return g.sink_tab && sum ? cuda_rc(launch_sink_sum(sg, g, dk, dv, bf16, status, st)) : BD_OK;
 }
 }  // namespace
 
@@ -524,8 +526,14 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
     return bwd_main_impl(dout, q, k, v, lse, seg, gi, n_sink, grad_dtype, dk, dv, workspace, dqf, status, stream);
   }
   if (int rc = bwd_prep_impl(dout, out, gi, workspace, nullptr, status, stream)) return rc;
-  if (int rc = bwd_main_impl(dout, q, k, v, lse, seg, gi, n_sink, grad_dtype, dk, dv, workspace, nullptr, status, stream))
+  if (int rc = bwd_main_impl(dout, q, k, v, lse, seg, gi, n_sink, grad_dtype, dk, dv, workspace, nullptr, status, stream,
+                             false))
     return rc;
+  if (g.sink_tab) {  // the partials' sums and dq's rounding in one launch
+    set_sink_part(&g, workspace);
+    return cuda_rc(launch_sink_finalize(static_cast<const int32_t*>(seg), g, dk, dv, workspace, dq, status,
+                                        static_cast<cudaStream_t>(stream)));
+  }
   return bd_attn_bwd_finalize(gi, grad_dtype, dq, workspace, status, stream);
 }
 }  // namespace

@@ -77,6 +77,19 @@ def test_parity(name, w, n, ranks):
         check_all(f"{name} r{r}", run(c, n), reference(c, n))
 
 
+@pytest.mark.parametrize("det", [False, True])
+@pytest.mark.parametrize("D,Hkv", [(64, 8), (128, 8), (256, 8), (512, 2)])
+def test_long_documents_over_many_tiles(D, Hkv, det):
+    """Tiles for most SMs, so that only the rows behind a sink tile's first unit are cut off, and bf16
+    gradients, which end in one launch."""
+    c = make_case(W(1, Hkv, Hkv, D, 2304, 3, ("explicit", (1000, 1250), 54), 130), 2, seed=6)
+    ref = reference(c, 5)
+    check_all("coarse", run(c, 5, torch.bfloat16, det=det), ref, torch.bfloat16)
+    c = make_case(W(1, Hkv, Hkv, D, 1800, 1, ("explicit", (20, 1700), 80), 200), 0, seed=7)
+    ref = reference(c, 70)
+    check_all("coarse 70", run(c, 70, det=det), ref)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
 def test_bf16_gradients_and_token_major(D):
     c = make_case(W(2, 4, 2, D, 900, 2, ("uniform", 50, 600, 30), 140), 1, seed=3)
