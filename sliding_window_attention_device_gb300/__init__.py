@@ -6,12 +6,14 @@ binding and :mod:`.synth` draws seeded synthetic inputs.
 """
 from importlib import import_module
 
-__all__ = ["bdattn", "synth", "bd_attn_seg_build", "bd_attn_fwd", "bd_attn_bwd"]
+_ENTRIES = ("bd_attn_seg_build", "bd_attn_fwd", "bd_attn_bwd", "bd_attn_sink_seg_build", "bd_attn_sink_fwd",
+            "bd_attn_sink_bwd", "bd_attn_paged_append", "bd_attn_paged_decode")
+__all__ = ["bdattn", "synth", *_ENTRIES]
 
 
 def __getattr__(name):
     if name in ("bdattn", "synth"):
         return import_module(f"{__name__}.{name}")
-    if name in ("bd_attn_seg_build", "bd_attn_fwd", "bd_attn_bwd"):
+    if name in _ENTRIES:
         return getattr(import_module(f"{__name__}.bdattn"), name)
     raise AttributeError(name)

@@ -22,6 +22,11 @@
 // masks over the tile's q columns before S arrives; the dropped weights are
 // zeroed in P^T (the dV operand), dS = P (Z dP - delta) takes the same
 // decisions, and dV is scaled by the keep scale when it is written.
+// With sinks (kSink) a CTA's work is a unit of a sink table (common.cuh): a K/V
+// tile, some of its q rows, some or all of the group's heads; a tile with several
+// units leaves fp32 shares that sink_kernels.cu adds. 2 x 32 heads x 4096 rows,
+// D 128, window 512, 4 sinks: 282 us with the sums; 2 x 6 heads x 333 rows, D 64:
+// one CTA per tile 29 us, cut to an SM's share of the steps 16 with the sums.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>

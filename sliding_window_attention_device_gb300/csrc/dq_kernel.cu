@@ -17,6 +17,8 @@
 // D = 256 and 512 stream K/V through a chunk ring (dq256_kernel.cu, dq512_kernel.cu).
 // With attention dropout (kDrop) each row draws its keep mask of a K/V tile
 // (dropout.cuh) before the tile's S and dP arrive: dS = P (Z dP - delta).
+// With sinks (kSink) the walk starts with the first document's sinks (sink_passes
+// in common.cuh), as tiles of their own.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>

@@ -21,6 +21,9 @@
 // With attention dropout (kDrop) each row draws its keep mask of a tile before
 // the tile's S arrives and zeroes the dropped weights of P; the keep scale is
 // folded into the final normalisation.
+// With sinks (kSink) the q tile first walks its first document's sinks, in passes
+// of 32 keys where they fit (sink_passes in common.cuh): 16 heads x 8192 rows,
+// window 1024, 4 sinks 162 us against 150 without.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>

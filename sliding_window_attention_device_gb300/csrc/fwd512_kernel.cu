@@ -19,6 +19,9 @@
 // both passes) before the tile's S arrives, zeroes the dropped weights of the
 // P it hands to the PV products (the row sum stays the undropped one) and
 // folds the keep scale into the scale of each O half.
+// With sinks (kSink) both walks over the K/V tiles start with the first document's
+// sinks, in passes of 32 keys where they fit (sink_passes in common.cuh): 16
+// heads x 2048 rows, window 1024, 16 sinks 165 us against 142 without.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>

@@ -5,19 +5,24 @@
 // (NeMo AutoModel API): padding is a contiguous tail so the real local rows
 // are a prefix [0, n_real); one varlen segment per document the local rows
 // touch, q segment = its local rows, k segment = [doc_start, last local q + 1).
-// Only the first segment can start before the shard (the straddle), so its
-// document start is found by scanning left; every later segment starts inside
-// the shard. The reference builds this on the host after a .tolist() copy;
-// here one CTA per batch row builds it on the device with warp ballots and a
-// block scan, so no host synchronisation is needed.
+// Only the first segment can start before the shard (the straddle); every later
+// segment starts inside it. The reference builds this on the host after a
+// .tolist() copy; here one CTA per batch row builds it on the device, so no host
+// synchronisation is needed: one pass over the row for the layout, the padding
+// and the straddle, two over the local rows that count and place the segments
+// with warp ballots. A chain of trips to L2 and block barriers bounds it, not the
+// bytes: as few of both as the steps' order allows, and blocks no wider than the
+// row needs. K1 and K2 together 5.5 us at 256 positions, 8 at 2 x 4096, 12 at
+// 16384 (12, 22 and 26 with a block scan and a binary search per row and tile).
 //
 // K2 marks every (128-row q tile, 128-row K/V tile) as full, partial or empty.
 // A real row p may attend the keys [lo(p), p] with lo(p) = max(doc_start(p),
 // p - W + 1); lo and hi are non-decreasing in p, so the non-empty K/V tiles
 // of a q tile form one contiguous range, and so do the q rows of a K/V tile.
 // The forward and backward kernels only visit those ranges (empty tiles are
-// never loaded) and mask only the partial tiles.
-#include <climits>
+// never loaded) and mask only the partial tiles. Tables with sinks also list the
+// backward's units (common.cuh), in a CTA beside the classification's two: 1 to 3
+// us more.
 #include <cstdint>
 
 #include "common.cuh"

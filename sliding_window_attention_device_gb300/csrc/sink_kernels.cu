@@ -2,11 +2,14 @@
 // several units of a K/V tile touch (see common.cuh).
 //
 // A sink's gradient sums over every later row of its document, so the backward
-// cuts those rows into units; each leaves its fp32 share of the at most n_sink
-// shared key rows in a slot of the workspace. Here every such row is the sum of
-// its tile's slots, added in slot order -- the same order in every run, no
-// atomics -- and rounded once to the gradient type. The traffic is n_sink rows
-// per unit and kv head; the cost is the launch.
+// cuts those rows into units (and, where the tiles are too few for the SMs, all
+// rows and the heads); each leaves its fp32 share of the shared key rows in a
+// slot of the workspace. Here every such row is the sum of its tile's slots,
+// added in slot order -- the same order in every run, no atomics -- and rounded
+// once to the gradient type. With n_sink rows per unit the cost is the launch; a
+// finely cut backward moves whole 128-row tiles through L2. A backward with bf16
+// gradients does it in the launch that rounds dq (359 -> 349 us at 2 x 32 heads x
+// 4096 rows, D 128).
 #include <cuda_bf16.h>
 #include <cstdint>
 
