@@ -18,8 +18,8 @@ namespace bd {
 // One CTA copies `tok` consecutive tokens: the first threads find each token's
 // sequence (binary search in cu_new), page and cache row, then all copy
 // 16-byte pieces, K and V together. Reads and writes every new element once: the
-// bytes bound it. 19,200 tokens of 12 prompts (8 kv heads, D 128, 157 MB in all)
-// 24 us, 6.5 TB/s; 64 single tokens 2.9 us, a launch's cost.
+// bytes bound it. 19,200 tokens of 12 prompts (8 kv heads, D 128, 157 MB in all),
+// new data each time: 27 us, 5.8 TB/s; 64 single tokens 3 us, a launch's cost.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTok = 16;
 
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     const int i = x / vpt, y = x - i * vpt, hk = y / vpr;
     const uint32_t row = s_row[i];
     if (row == 0xffffffffu) continue;
-    const uint4 kk = __ldcs(k_new + src0 + x), vv = __ldcs(v_new + src0 + x);
+    const uint4 kk = __ldg(k_new + src0 + x), vv = __ldg(v_new + src0 + x);
     const size_t dst = (static_cast<size_t>(row) + static_cast<size_t>(hk) * g.page_size) * vpr + (y - hk * vpr);
     k_pages[dst] = kk;
     v_pages[dst] = vv;
@@ -82,9 +82,13 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int3
                                 const int32_t* page_table, const PagedGeom& g, int n_tokens, void* k_pages,
                                 void* v_pages, int32_t* status, cudaStream_t st) {
   if (n_tokens == 0) return cudaSuccess;
-  // a token per CTA until the CTAs fill the machine four times over
+  // a token per CTA until the CTAs fill the machine four times over; then two
+  // pieces of K and of V per thread (at 8 kv heads, D 128, 19,200 tokens: 1 token
+  // a CTA 33 us, 2 28, 4 27, 8 27.5, 16 29.5)
+  int most = 2 * kAppendThreads / (g.Hkv * (g.D / 8));
+  most = most < 1 ? 1 : most > kAppendTok ? kAppendTok : most;
   int tok = (n_tokens + 4 * kSms - 1) / (4 * kSms);
-  tok = tok < 1 ? 1 : tok > kAppendTok ? kAppendTok : tok;
+  tok = tok < 1 ? 1 : tok > most ? most : tok;
   const unsigned grid = static_cast<unsigned>((n_tokens + tok - 1) / tok);
   if (const cudaError_t le =
           launch_pdl(paged_append_kernel, dim3(grid), dim3(kAppendThreads), 0, st, static_cast<const uint4*>(k_new),
