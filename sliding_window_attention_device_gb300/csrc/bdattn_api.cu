@@ -132,7 +132,8 @@ int to_geom(const bd_geom* in, Geom* g) {
   g->row_offset = in->row_offset;
   g->kv_offset = in->kv_offset;
   g->S_kv = in->S_kv;
-  g->window = in->window > 0 ? in->window : 0;
+  // a window beyond every distance is clamped, so that position + window stays within 32 bits
+  g->window = in->window > (1 << 29) ? 1 << 29 : in->window > 0 ? in->window : 0;
   g->scale = in->scale > 0.f ? in->scale : 1.0f / std::sqrt(static_cast<float>(in->D));
   g->kv_tm = in->kv_layout == BD_KV_SBHD;
   seg_layout(g->B, g->L, g->S_kv, g->off, &g->nqt, &g->nkt, &g->nkw);

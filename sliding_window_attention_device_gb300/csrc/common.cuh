@@ -196,10 +196,9 @@ __host__ __device__ inline long long sink_words(const Geom& g) {
 // *nx). A q tile walks these first, seeing that document's sinks only, then its
 // window's tiles, seeing the window only (and, for W < kTile, the sinks of the
 // documents that start inside it: RowKeys); a tile may come up in both walks.
-// Where a sink
-// tile's sinks fit 32 columns from a 16-column boundary on, col[] is the first of
-// them and the pass works on 32 keys instead of 128, else -1. ds: the document
-// start of the q tile's first row (row_lo).
+// Where a sink tile's sinks fit 32 columns from a 16-column boundary on, col[] is
+// the first of them and the pass works on 32 keys instead of 128, else -1. ds:
+// the document start of the q tile's first row (row_lo).
 __device__ inline void sink_passes(const Geom& g, int ds, int qt, int n_real, int* x0, int* nx, int* col) {
   *x0 = *nx = 0;
   col[0] = col[1] = -1;

@@ -116,6 +116,8 @@ DECODE = [
     ("window1", [1, 2, 50], 2, 2, 64, 16, 1, 0),
     ("window1_sink1", [1, 2, 50], 2, 2, 64, 16, 1, 1),
     ("sinks_past_window", [50, 300, 1000], 4, 2, 128, 16, 64, 200),
+    ("window_and_sinks_of_any_size", [50, 700], 4, 2, 128, 16, 2 ** 31 - 1, 2 ** 31 - 1),
+    ("sinks_of_any_size", [50, 700], 4, 2, 128, 16, 60, 2 ** 31 - 1),
     ("d256", [2000, 0, 700, 1], 8, 4, 256, 16, 512, 4),
     ("d512", [900, 33, 16], 8, 2, 512, 64, 0, 0),
     ("long_split", [20011], 8, 1, 128, 64, 0, 0),

@@ -337,3 +337,22 @@ def test_ids_in_any_order():
     doc[0, :20] = doc[0, 500]  # a local document's id before its run
     _, status = bdattn.bd_attn_sink_seg_build(torch.from_numpy(doc).cuda(), g, 4)
     assert int(status.item()) == bdattn.STATUS_LAYOUT
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_window_of_any_size(D):
+    """A window of 2^31 - 1: position + window must not wrap, with sinks and without."""
+    c = make_case(W(1, 2, 1, D, 500, 2, ("explicit", (40, 420), 40), 2 ** 31 - 1), 1, seed=8)
+    cc = dict(c)
+    cc["window"] = 0
+    ref = reference(cc, 0)
+    check_all("sinks", run(c, 4), ref)
+    check_all("none", run(c, 0), ref)
+    g = gpu_geom(c)
+    dev = torch.device("cuda")
+    q, k, v, do = (c[x].to(dev) for x in ("q", "k", "v", "do"))
+    seg, status = bdattn.bd_attn_seg_build(torch.from_numpy(c["doc"]).to(dev), g)
+    out, lse = bdattn.bd_attn_fwd(q, k, v, seg, g, status)
+    dq, dk, dv = bdattn.bd_attn_bwd(do, q, k, v, out, lse, seg, g, status)
+    assert int(status.item()) == 0
+    check_all("ordinary", dict(out=out, lse=lse, dq=dq, dk=dk, dv=dv), ref)
