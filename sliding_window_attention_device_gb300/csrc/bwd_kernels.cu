@@ -23,6 +23,13 @@
 // exact and deterministic. For D = 256 the dK / dV columns are produced in
 // two passes of 128 (the S / dP products are recomputed in the second pass)
 // because 2 x 256 fp32 columns would fill the whole tensor memory.
+// K and V resident leave room for one q tile of Q and dO and half a Q more. Each
+// half is refilled as soon as its last product is done, and the next tile's S^T
+// is issued before this tile's dK and dQ^T, so that it runs while dS is formed:
+// 412 TFLOP/s against 363 with Q and dO freed together (16 q heads, 8 kv heads,
+// 65,536 rows over 8 shards, window 1024), and 857 against 955 us with 4 sinks
+// (8192 rows, 16 heads, window 1024). What is left is S and dP formed twice and
+// the chain S, P, dS, dQ within a tile.
 //   warp 0  loads (TMA for K, V, Q, dO; the q rows' lse / delta / mask bounds)
 //   warp 1  issues the MMAs          warp 2  owns the tensor memory
 //   warps 4-7 and 12-15  P, dS (thread = key row; q columns 0-31 / 32-63)
@@ -121,7 +128,6 @@ template <int D>
 struct BwdCfg {
   static constexpr int kDp = D < 128 ? D : 128;  // dK / dV columns per pass
   static constexpr int kPasses = D / kDp;
-  static constexpr int kNsq = D == 256 ? 1 : (D == 128 ? 3 : 4);  // Q / dO stages
   // dQ^T is double-buffered in tensor memory: columns [128,192) and [192,256).
   static constexpr uint32_t kColS = 0, kColDp = 64, kColDq = 128, kColDv = 256, kColDk = 384;
   // For D <= 128 the dq partial tile is staged in shared memory (64 q x 64 d
@@ -139,25 +145,30 @@ struct DqStage {
 template <>
 struct DqStage<0> {};
 
-template <int D, int NSQ>
+template <int D>
 struct BwdSmem {
   static constexpr int kChunks = D / 64;
   static constexpr int kKChunk = kTile * 128;  // 128 rows x 128 B
   static constexpr int kQChunk = kBwdQ * 128;  // 64 rows x 128 B
+  static constexpr int kHalf = kChunks / 2;    // 64-column chunks of half the head dim
   // v must directly follow k: for D = 64 the dQ^T product reads A rows
   // 64..127 (d >= 64, discarded) from the 16 KB after k.
   alignas(1024) uint8_t k[kChunks][kKChunk];
   alignas(1024) uint8_t v[kChunks][kKChunk];
-  alignas(1024) uint8_t q[NSQ][kChunks][kQChunk];
-  alignas(1024) uint8_t dout[NSQ][kChunks][kQChunk];
+  // The q tile's Q and dO in halves of the head dim: the one whose dV / dK columns
+  // this pass produces (late) and the other (early), which only S and dP read.
+  alignas(1024) uint8_t q_early[kHalf][kQChunk];
+  alignas(1024) uint8_t q_late[2][kHalf][kQChunk];  // by tile parity
+  alignas(1024) uint8_t do_early[kHalf][kQChunk];
+  alignas(1024) uint8_t do_late[kHalf][kQChunk];
   alignas(1024) uint8_t ds[kKChunk];  // dS^T, 128 keys x 64 q, bf16, 128B-swizzled
   DqStage<BwdCfg<D>::kStageSlots> stage;
   alignas(16) float lse2[2][kBwdQ];  // per q row: lse * log2(e), by tile parity
   alignas(16) float delta[2][kBwdQ];
-  // the Q / dO stage in two groups (chunks [g kDp/64, (g+1) kDp/64) of both):
-  // a tile frees the group its dK / dV products do not read as soon as its S
-  // and dP products are done, so the next tile's copy of it starts early
-  uint64_t kv_full, grp_full[2], grp_empty[2];
+  // Each half is refilled as soon as its last product is done: the early Q after
+  // S, the early dO after dP, the late dO after dV; the late Q, which dK reads
+  // last of all, has two buffers. So the next tile's S runs while dS is formed.
+  uint64_t kv_full, qe_full, qe_empty, ql_full[2], ql_empty[2], de_full, de_empty, dl_full, dl_empty;
   uint64_t s_full, dp_full, p_full, ds_full, ds_empty, dq_full[2], dq_empty[2], acc_full, acc_empty, mma_drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -182,10 +193,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                void* __restrict__ dk, void* __restrict__ dv, int grads_bf16, int32_t* status) {
   pdl_begin();
   using Cfg = BwdCfg<D>;
-  constexpr int NSQ = Cfg::kNsq, kDp = Cfg::kDp, kPasses = Cfg::kPasses;
-  static_assert(NSQ == 1 && kPasses == 2, "one Q / dO stage in two groups, two passes over D (D = 256)");
-  constexpr int kGrp = kDp / 64;  // 64-column chunks per group
-  using Smem = BwdSmem<D, NSQ>;
+  constexpr int kDp = Cfg::kDp, kPasses = Cfg::kPasses;
+  static_assert(kPasses == 2, "two passes over the halves of D (D = 256)");
+  using Smem = BwdSmem<D>;
+  constexpr int kHalf = Smem::kHalf;
+  static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory per CTA");
   constexpr int kChunks = Smem::kChunks;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned base, derived from smem_raw so the compiler keeps the shared address space
@@ -267,9 +279,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     s.skip = (!ok || before != 0) ? 1 : 0;
     s.abort_flag = 0;
     mbar_init(&s.kv_full, 1);
+    mbar_init(&s.qe_full, 1);
+    mbar_init(&s.qe_empty, 1);
+    mbar_init(&s.de_full, 1);
+    mbar_init(&s.de_empty, 1);
+    mbar_init(&s.dl_full, 1);
+    mbar_init(&s.dl_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.grp_full[i], 1);
-      mbar_init(&s.grp_empty[i], 1);
+      mbar_init(&s.ql_full[i], 1);
+      mbar_init(&s.ql_empty[i], 1);
     }
     mbar_init(&s.s_full, 1);
     mbar_init(&s.dp_full, 1);
@@ -347,13 +365,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tma_load_3d(s.v[c], &tm_v, &s.kv_full, c * 64, g.kv_tm ? b * g.Hkv + hk : kt * kTile, g.kv_tm ? kt * kTile : b * g.Hkv + hk);
       }
     }
-    int issued[2] = {0, 0};
+    int n_qe = 0, n_ql = 0, n_de = 0, n_dl = 0;  // halves issued
     bool stopped = false;
-    for (int it = 0; it < n_it && !stopped; ++it) {
+    // half `hf` of the head dim of the tile's Q or dO into a buffer (lane 0)
+    auto load_half = [&](uint8_t (*dst)[Smem::kQChunk], const CUtensorMap* map, uint64_t* bar, int hf, int q0, int pl) {
+      mbar_arrive_expect_tx(bar, kHalf * Smem::kQChunk);
+      for (int c = 0; c < kHalf; ++c) tma_load_3d(dst[c], map, bar, (hf * kHalf + c) * 64, q0, pl);
+    };
+    for (int it = 0; it < n_it; ++it) {
       int pass, h, q0;
       decode(it, pass, h, q0);
-      // the per-row values are fetched before waiting for the free stage so
-      // that their global-load latency overlaps the wait
+      const int qpl = b * g.Hq + h, st = it & 1;
+      // the per-row values are fetched before the waits so that their
+      // global-load latency overlaps them
       float l2[2], dl[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -366,33 +390,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           dl[e] = delta[row] * g.scale;  // dS is formed pre-scaled: scale * P (dP - delta)
         }
       }
-      // the group the previous tile freed early first, then the other
-      const int ge = it > 0 ? 1 - (it - 1) / n_it_pass : 0;
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        const int gr = k == 0 ? ge : 1 - ge;
-        if (it > 0 && !warp_wait(&s.grp_empty[gr], (it - 1) & 1, &s.abort_flag, vstatus)) {
-          stopped = true;
-          break;
-        }
-        if (k == 0) {  // this tile's row values (slot it & 1: tile it - 2's, read long before)
+      // in the order the buffers come free: after S(it - 1), dK(it - 2), dP(it - 1), dV(it - 1)
+      stopped = true;
+      if (it > 0 && !warp_wait(&s.qe_empty, (it - 1) & 1, &s.abort_flag, vstatus)) break;
+      if (lane == 0) load_half(s.q_early, &tm_q, &s.qe_full, 1 - pass, q0, qpl);
+      ++n_qe;
+      if (it > 1 && !warp_wait(&s.ql_empty[st], ((it >> 1) - 1) & 1, &s.abort_flag, vstatus)) break;
+      // the row values with the late Q, whose barrier publishes them: slot st's
+      // readers, tile it - 2's, formed their dS before the dK just waited for
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = lane + 32 * e;
-            s.lse2[it & 1][c] = l2[e];
-            s.delta[it & 1][c] = dl[e];
-          }
-          __syncwarp();
-        }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&s.grp_full[gr], 2 * kGrp * Smem::kQChunk);
-          for (int c = gr * kGrp; c < (gr + 1) * kGrp; ++c) {
-            tma_load_3d(s.q[0][c], &tm_q, &s.grp_full[gr], c * 64, q0, b * g.Hq + h);
-            tma_load_3d(s.dout[0][c], &tm_dout, &s.grp_full[gr], c * 64, q0, b * g.Hq + h);
-          }
-        }
-        ++issued[gr];
+      for (int e = 0; e < 2; ++e) {
+        s.lse2[st][lane + 32 * e] = l2[e];
+        s.delta[st][lane + 32 * e] = dl[e];
       }
+      __syncwarp();
+      if (lane == 0) load_half(s.q_late[st], &tm_q, &s.ql_full[st], pass, q0, qpl);
+      ++n_ql;
+      if (it > 0 && !warp_wait(&s.de_empty, (it - 1) & 1, &s.abort_flag, vstatus)) break;
+      if (lane == 0) load_half(s.do_early, &tm_dout, &s.de_full, 1 - pass, q0, qpl);
+      ++n_de;
+      if (it > 0 && !warp_wait(&s.dl_empty, (it - 1) & 1, &s.abort_flag, vstatus)) break;
+      if (lane == 0) load_half(s.do_late, &tm_dout, &s.dl_full, pass, q0, qpl);
+      ++n_dl;
+      stopped = false;
     }
     if (lane == 0) {
       if (stopped) {
@@ -401,8 +421,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       // no copy into this CTA's shared memory may still be in flight at exit
       mbar_wait_drain(&s.kv_full, 0);
-      for (int gr = 0; gr < 2; ++gr)
-        if (issued[gr] > 0) mbar_wait_drain(&s.grp_full[gr], (issued[gr] - 1) & 1);
+      if (n_qe > 0) mbar_wait_drain(&s.qe_full, (n_qe - 1) & 1);
+      if (n_de > 0) mbar_wait_drain(&s.de_full, (n_de - 1) & 1);
+      if (n_dl > 0) mbar_wait_drain(&s.dl_full, (n_dl - 1) & 1);
+      for (int x = (n_ql > 2 ? n_ql - 2 : 0); x < n_ql; ++x) mbar_wait_drain(&s.ql_full[x & 1], (x >> 1) & 1);
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
@@ -414,44 +436,49 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint64_t dMN_q = umma_desc_sw128(0, Smem::kQChunk, 1024);      // MN-major, 64-row chunks
       const uint64_t dMN_k = umma_desc_sw128(0, Smem::kKChunk, 1024);      // MN-major, 128-row chunks
       const uint32_t a_k = smem_u32(s.k[0]), a_v = smem_u32(s.v[0]), a_ds = smem_u32(s.ds);
-      const uint32_t a_q = smem_u32(s.q[0][0]), a_do = smem_u32(s.dout[0][0]);
-      // X^T = A B^T over the head-dim chunks of group gr (A = K or V, B = Q or dO)
-      auto issue_grp = [&](uint32_t col, uint32_t a_base, uint32_t b_base, int gr, bool first) {
+      const uint32_t a_qe = smem_u32(s.q_early[0]), a_ql = smem_u32(s.q_late[0][0]);
+      const uint32_t a_de = smem_u32(s.do_early[0]), a_dl = smem_u32(s.do_late[0]);
+      constexpr uint32_t kHalfBytes = kHalf * Smem::kQChunk;
+      auto wait = [&](uint64_t* bar, uint32_t par) { return pipe_wait(bar, par, &s.abort_flag, vstatus); };
+      // X^T (+)= A B^T over half hf of the head dim (A = K or V; B: the half's buffer of Q or dO)
+      auto issue_half = [&](uint32_t col, uint32_t a_base, uint32_t bb, int hf, bool first) {
 #pragma unroll
-        for (int kk = 0; kk < 4 * kGrp; ++kk) {
-          const int ks = gr * 4 * kGrp + kk;
-          const uint32_t off_a = (ks >> 2) * Smem::kKChunk + (ks & 3) * 32;
-          const uint32_t off_b = (ks >> 2) * Smem::kQChunk + (ks & 3) * 32;
-          umma_ss(tbase + col, desc_at(dK_major, a_base + off_a), desc_at(dK_major, b_base + off_b), idST,
+        for (int kk = 0; kk < 4 * kHalf; ++kk) {
+          const uint32_t off_a = (hf * kHalf + (kk >> 2)) * Smem::kKChunk + (kk & 3) * 32;
+          const uint32_t off_b = (kk >> 2) * Smem::kQChunk + (kk & 3) * 32;
+          umma_ss(tbase + col, desc_at(dK_major, a_base + off_a), desc_at(dK_major, bb + off_b), idST,
                   (first && kk == 0) ? 0u : 1u);
         }
       };
-      auto wait = [&](uint64_t* bar, uint32_t par) { return pipe_wait(bar, par, &s.abort_flag, vstatus); };
-      // S^T and dP^T of tile t: the group the previous tile freed early (and
-      // whose copy started first) first; then the group tile t's dK / dV do not
-      // read is free again once these are done
-      auto issue_sdp = [&](int t) -> bool {
-        const int ge = t > 0 ? 1 - (t - 1) / n_it_pass : 0, gl = 1 - ge;
-        if (!wait(&s.grp_full[ge], t & 1)) return false;
+      // both halves; the first tile of a pass sums its late half first, the others their early one
+      auto issue_both = [&](uint32_t col, uint32_t a_base, uint32_t early, uint32_t late, int t) {
+        const int pass = t / n_it_pass;
+        const bool late_first = t % n_it_pass == 0;
+        issue_half(col, a_base, late_first ? late : early, late_first ? pass : 1 - pass, true);
+        issue_half(col, a_base, late_first ? early : late, late_first ? 1 - pass : pass, false);
+      };
+      auto issue_s = [&](int t) -> bool {
+        if (!wait(&s.qe_full, t & 1) || !wait(&s.ql_full[t & 1], (t >> 1) & 1)) return false;
         tc_fence_after();
-        issue_grp(Cfg::kColS, a_k, a_q, ge, true);
-        issue_grp(Cfg::kColDp, a_v, a_do, ge, true);
-        if (!wait(&s.grp_full[gl], t & 1)) return false;
-        tc_fence_after();
-        issue_grp(Cfg::kColS, a_k, a_q, gl, false);
+        issue_both(Cfg::kColS, a_k, a_qe, a_ql + (t & 1) * kHalfBytes, t);
         umma_commit(&s.s_full);
-        issue_grp(Cfg::kColDp, a_v, a_do, gl, false);
-        umma_commit(&s.dp_full);
-        umma_commit(&s.grp_empty[1 - t / n_it_pass]);
+        umma_commit(&s.qe_empty);
         return true;
       };
-      bool ok = wait(&s.kv_full, 0) && issue_sdp(0);
+      auto issue_dp = [&](int t) -> bool {
+        if (!wait(&s.de_full, t & 1) || !wait(&s.dl_full, t & 1)) return false;
+        tc_fence_after();
+        issue_both(Cfg::kColDp, a_v, a_de, a_dl, t);
+        umma_commit(&s.dp_full);
+        umma_commit(&s.de_empty);
+        return true;
+      };
+      bool ok = wait(&s.kv_full, 0) && issue_s(0) && issue_dp(0);
       for (int it = 0; ok && it < n_it; ++it) {
         int pass, h, q0;
         decode(it, pass, h, q0);
         const bool first_of_pass = (it % n_it_pass) == 0;
         const bool last_of_pass = (it % n_it_pass) == n_it_pass - 1;
-        const uint32_t pass_off_q = pass * kGrp * Smem::kQChunk;  // this pass's group of Q / dO chunks
         if (first_of_pass && pass > 0 && !wait(&s.acc_empty, (pass - 1) & 1)) { ok = false; break; }
         // dV += P^T dO[:, pass]; P^T is bf16 in tensor memory, q columns 0-31 at
         // column offset 0 and 32-63 at offset 48 (each half writes over its own S^T)
@@ -460,16 +487,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < kBwdQ / 16; ++ks) {
           const uint32_t a_col = Cfg::kColS + (ks < 2 ? ks * 8 : 48 + (ks - 2) * 8);
-          umma_ts(tbase + Cfg::kColDv, tbase + a_col, desc_at(dMN_q, a_do + pass_off_q + ks * 2048), idDKV,
+          umma_ts(tbase + Cfg::kColDv, tbase + a_col, desc_at(dMN_q, a_dl + ks * 2048), idDKV,
                   (!first_of_pass || ks > 0) ? 1u : 0u);
         }
+        umma_commit(&s.dl_empty);  // dP and dV of this tile are issued
+        // S^T of the next tile while dS is formed (the dV product above was issued
+        // first, so it reads P^T before S^T is overwritten)
+        if (it + 1 < n_it && !issue_s(it + 1)) { ok = false; break; }
         // dK += dS^T Q[:, pass] ; dQ^T = K[:, pass]^T dS^T
         if (!wait(&s.ds_full, it & 1)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < kBwdQ / 16; ++ks)
-          umma_ss(tbase + Cfg::kColDk, desc_at(dK_major, a_ds + ks * 32), desc_at(dMN_q, a_q + pass_off_q + ks * 2048),
-                  idDKV, (!first_of_pass || ks > 0) ? 1u : 0u);
+          umma_ss(tbase + Cfg::kColDk, desc_at(dK_major, a_ds + ks * 32),
+                  desc_at(dMN_q, a_ql + (it & 1) * kHalfBytes + ks * 2048), idDKV, (!first_of_pass || ks > 0) ? 1u : 0u);
+        umma_commit(&s.ql_empty[it & 1]);
         if constexpr (kDq) {
           const int bq = it & 1;  // dQ^T tensor-memory buffer
           if (it >= 2 && !wait(&s.dq_empty[bq], ((it >> 1) - 1) & 1)) { ok = false; break; }
@@ -482,12 +514,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           umma_commit(&s.dq_full[bq]);
         }
         umma_commit(&s.ds_empty);
-        umma_commit(&s.grp_empty[pass]);  // this pass's group: read by dV, dK above
         if (last_of_pass) umma_commit(&s.acc_full);
-        if (it + 1 < n_it && !issue_sdp(it + 1)) {
-          ok = false;
-          break;
-        }
+        // dP^T of the next tile (this one's was read before dS was formed)
+        if (it + 1 < n_it && !issue_dp(it + 1)) { ok = false; break; }
       }
       if (!ok) {
         s.abort_flag = 1;
@@ -557,9 +586,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint64_t km = 0;  // dropout: keep bits of this key over the half's 32 q columns
       if constexpr (kDrop)
         km = key_keep_mask<4>(g, b, h, g.row_offset + q0 + c0, g.kv_offset + kt * kTile + (warp & 3) * 32, lane);
-      // the early group's copy also publishes this tile's row values
-      const int ge = it > 0 ? 1 - (it - 1) / n_it_pass : 0;
-      if (!warp_wait(&s.grp_full[ge], it & 1, &s.abort_flag, vstatus)) { ok = false; break; }
+      // the late Q's copy also publishes this tile's row values; its barrier is not
+      // completed again before this tile's dS is in (a single one might be)
+      if (!warp_wait(&s.ql_full[st], (it >> 1) & 1, &s.abort_flag, vstatus)) { ok = false; break; }
       if (!warp_wait(&s.s_full, it & 1, &s.abort_flag, vstatus)) { ok = false; break; }
       tc_fence_after();
       uint32_t sr[32];
@@ -754,7 +783,7 @@ cudaError_t launch_main_d(const CUtensorMap& mq, const CUtensorMap& mdo, const C
                           const CUtensorMap& mv, const CUtensorMap& mdq, const int32_t* seg, const Geom& g, const float* lse,
                           const float* delta, float* dq_acc, void* dk, void* dv, int bf16, int32_t* status,
                           cudaStream_t st) {
-  const size_t smem = sizeof(BwdSmem<D, BwdCfg<D>::kNsq>) + 1024;  // + 1 KB to align the swizzled tiles
+  const size_t smem = sizeof(BwdSmem<D>) + 1024;  // + 1 KB to align the swizzled tiles
   auto kern = g.sink_tab ? (g.drop_t ? bwd_kernel<D, kDq, true, true> : bwd_kernel<D, kDq, false, true>)
                          : (g.drop_t ? bwd_kernel<D, kDq, true, false> : bwd_kernel<D, kDq, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
