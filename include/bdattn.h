@@ -328,6 +328,9 @@ int bd_attn_bwd_noalloc(const void* dout, const void* q, const void* k, const vo
  * window and kt_qrange covering the rows that reach a tile through its sinks
  * too. A table belongs to the n_sink it was built for: the kernels set
  * BD_STATUS_BOUNDS for another one's (ordinary entry points take only n_sink 0).
+ * The backward's work is also cut for B, Hq, Hkv and D: a backward whose cut
+ * would differ sets BD_STATUS_BOUNDS too (the forward takes the table of any
+ * heads and head dim).
  *
  * As in the other entry points, every q, k, v and dout row must hold finite
  * values, masked or not (a masked weight is a zero that is multiplied). */

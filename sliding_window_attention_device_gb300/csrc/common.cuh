@@ -63,7 +63,8 @@ constexpr int kHdrRowOffset = 16, kHdrL = 17, kHdrKvOffset = 18, kHdrSkv = 19, k
               kHdrSfull = 21, kHdrMagic = 22,
               kHdrKvChunk = 23,  // 1: table built for one K/V chunk (no K/V range requirement)
               kHdrSink = 24,     // n_sink the table was built for (0 in ordinary tables)
-              kHdrSinkTab = 25;  // 1: the sink regions follow the table
+              kHdrSinkTab = 25,  // 1: the sink regions follow the table
+              kHdrSinkCut = 28;  // and what these were laid out for: B, G, sk_units, sk_rows
 constexpr int kSegMagic = 0x62646174;  // "bdat"
 
 // Whether a batch row's header was written for this geometry: three 16-byte
@@ -249,13 +250,18 @@ __device__ __forceinline__ uint32_t keep_bits32(const uint32_t (&km)[4], int c0)
   return (c0 & 16) ? (lo >> 16) | (hi << 16) : lo;
 }
 
-// Units of a sink table, or -1 when the table is not one for this geometry
-// (the regions' places follow from it).
+// Units of a sink table, or -1 when the table is not one for this geometry. The
+// regions' places and the units' heads, rows and slots follow from the batch and
+// the heads too, which the ordinary table does not depend on; with B, G, sk_units
+// and sk_rows alike and the counts within capacity the units say the rest.
 __device__ __forceinline__ int sink_n_units(const Geom& g, const int32_t* seg) {
   const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR];
-  if (!seg_hdr_ok(g, hdr) || hdr[kHdrSinkTab] != 1) return -1;
-  const int n = seg[g.sk_off];
-  return n <= g.sk_units ? n : -1;
+  const int4 cut = *reinterpret_cast<const int4*>(hdr + kHdrSinkCut);
+  if (!seg_hdr_ok(g, hdr) || hdr[kHdrSinkTab] != 1 || cut.x != g.B || cut.y != g.G || cut.z != g.sk_units ||
+      cut.w != g.sk_rows)
+    return -1;
+  const int4 n = *reinterpret_cast<const int4*>(seg + g.sk_off);
+  return n.x <= g.sk_units && n.y <= g.sk_sums && n.z <= g.sk_slots ? n.x : -1;
 }
 
 // Where key row r of a unit's tile goes: >= 0 a row of the unit's partial slot,

@@ -297,7 +297,9 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
     hdr[kHdrMagic] = kSegMagic;
     hdr[kHdrSink] = g.n_sink;
     hdr[kHdrSinkTab] = g.sink_tab;
-    for (int x = kHdrSinkTab + 1; x < BD_SEG_HDR_WORDS; ++x) hdr[x] = 0;
+    const int cut[4] = {g.B, g.G, g.sk_units, g.sk_rows};
+    for (int x = kHdrSinkTab + 1; x < BD_SEG_HDR_WORDS; ++x)
+      hdr[x] = g.sink_tab && x >= kHdrSinkCut ? cut[x - kHdrSinkCut] : 0;
     if (row_status) atomicOr(status, row_status);
   }
 }
