@@ -395,11 +395,11 @@ typedef struct {
 
 /* Write new tokens into their sequences' pages. k_new, v_new: bf16
  * [n_tokens, Hkv, D], sequence after sequence: sequence b's are
- * [cu_new[b], cu_new[b+1]) (int32 [B+1], cu_new[0] = 0, cu_new[B] <= n_tokens)
- * and its last one goes to position seq_lens[b] - 1. Rows from cu_new[B] on are
- * padding. A token whose page is -1 is dropped (with a window, a long prompt's
- * tokens that no later token sees need no page). No two tokens may share a
- * place in the cache. */
+ * [cu_new[b], cu_new[b+1]) (int32 [B+1] that never falls, cu_new[0] = 0,
+ * cu_new[B] <= n_tokens, else BD_STATUS_BOUNDS) and its last one goes to position
+ * seq_lens[b] - 1. Rows from cu_new[B] on are padding. A token whose page is -1
+ * is dropped (with a window, a long prompt's tokens that no later token sees need
+ * no page). No two tokens may share a place in the cache. */
 int bd_attn_paged_append(const void* k_new, const void* v_new, const int32_t* cu_new, const int32_t* seq_lens,
                          const int32_t* page_table, const bd_paged* g, int n_tokens, void* k_pages, void* v_pages,
                          int32_t* status, bd_stream_t stream);

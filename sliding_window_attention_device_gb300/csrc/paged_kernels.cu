@@ -32,10 +32,11 @@ __global__ void __launch_bounds__(kAppendThreads)
   __shared__ uint32_t s_row[kAppendTok];  // cache row of kv head 0, or 0xffffffff: not stored
   __shared__ int s_skip;
   const int t0 = blockIdx.x * tok;
-  if (threadIdx.x == 0) {
-    s_skip = *reinterpret_cast<const volatile int*>(status) != 0;
-    if (blockIdx.x == 0 && (cu_new[0] != 0 || cu_new[g.B] > n_tokens || cu_new[g.B] < 0))
-      atomicOr(status, BD_STATUS_BOUNDS);
+  if (threadIdx.x == 0) s_skip = *reinterpret_cast<const volatile int*>(status) != 0;
+  if (blockIdx.x == 0) {  // the offsets as a whole: from 0, never falling, to n_tokens at most
+    bool bad = threadIdx.x == 0 && (cu_new[0] != 0 || cu_new[g.B] > n_tokens);
+    for (int x = threadIdx.x; x < g.B; x += kAppendThreads) bad |= cu_new[x + 1] < cu_new[x];
+    if (bad) atomicOr(status, BD_STATUS_BOUNDS);
   }
   if (threadIdx.x < static_cast<unsigned>(tok)) {
     const int t = t0 + static_cast<int>(threadIdx.x);
@@ -46,10 +47,13 @@ __global__ void __launch_bounds__(kAppendThreads)
         const int mid = (a + e + 1) >> 1;
         if (cu_new[mid] <= t) a = mid; else e = mid - 1;
       }
-      const int end = cu_new[a + 1];
-      if (cu_new[a] <= t && t < end) {
+      const int begin = cu_new[a], end = cu_new[a + 1];
+      if (begin <= t && t < end) {
+        // among offsets that fall, a range that reaches past all new tokens is no
+        // sequence's: its tokens would go to places of earlier ones
         const long long pos = static_cast<long long>(seq_lens[a]) - (end - t);
-        int bad = pos < 0 || pos >= static_cast<long long>(g.max_pages) * g.page_size;
+        int bad = begin < 0 || end > min(cu_new[g.B], n_tokens) || pos < 0 ||
+                  pos >= static_cast<long long>(g.max_pages) * g.page_size;
         if (!bad) {
           int off;
           const int page = page_of(g, page_table, a, static_cast<int>(pos), &off);
@@ -81,7 +85,6 @@ __global__ void __launch_bounds__(kAppendThreads)
 cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int32_t* cu_new, const int32_t* seq_lens,
                                 const int32_t* page_table, const PagedGeom& g, int n_tokens, void* k_pages,
                                 void* v_pages, int32_t* status, cudaStream_t st) {
-  if (n_tokens == 0) return cudaSuccess;
   // a token per CTA until the CTAs fill the machine four times over; then two
   // pieces of K and of V per thread (at 8 kv heads, D 128, 19,200 tokens: 1 token
   // a CTA 33 us, 2 28, 4 27, 8 27.5, 16 29.5)
@@ -89,7 +92,8 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int3
   most = most < 1 ? 1 : most > kAppendTok ? kAppendTok : most;
   int tok = (n_tokens + 4 * kSms - 1) / (4 * kSms);
   tok = tok < 1 ? 1 : tok > most ? most : tok;
-  const unsigned grid = static_cast<unsigned>((n_tokens + tok - 1) / tok);
+  // (no tokens: one CTA, for the offsets' check)
+  const unsigned grid = n_tokens == 0 ? 1u : static_cast<unsigned>((n_tokens - 1) / tok + 1);
   if (const cudaError_t le =
           launch_pdl(paged_append_kernel, dim3(grid), dim3(kAppendThreads), 0, st, static_cast<const uint4*>(k_new),
                      static_cast<const uint4*>(v_new), cu_new, seq_lens, page_table, g, n_tokens, tok,
