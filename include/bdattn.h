@@ -409,7 +409,8 @@ int bd_attn_paged_append(const void* k_new, const void* v_new, const int32_t* cu
  * out bf16 [B, Hq, D] and lse fp32 [B, Hq] (natural log), the rule of
  * bd_attn_sink_fwd. Only visible tokens' pages are read: behind the window the
  * table may hold anything, and a page's places behind the sequence may too. A
- * sequence of length 0 gets out = 0, lse = -inf. Results are bitwise
+ * sequence of length 0 gets out = 0, lse = -inf. A score of -inf weighs nothing;
+ * a NaN or +inf one makes its head's out and lse NaN. Results are bitwise
  * reproducible for the same lengths. workspace:
  * bd_attn_paged_decode_workspace_bytes bytes, 16-byte aligned, not shared by
  * calls that may overlap; NULL will do where that size is 16 (no row is split). */

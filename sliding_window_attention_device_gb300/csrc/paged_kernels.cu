@@ -199,6 +199,16 @@ __device__ __forceinline__ Visible visible_keys(const PagedGeom& g, const int32_
   return v;
 }
 
+// What exponents are taken against: the maximum, or 0 where every score so far
+// is -inf, whose weights are then 0 and not NaN.
+__device__ __forceinline__ float exp_base(float m) { return m == -INFINITY ? 0.f : m; }
+// O's factor and the log-sum-exp of a row with maximum m (log2) and sum l: out 0
+// and -inf where nothing weighs (l = 0), NaN where a score is.
+__device__ __forceinline__ float row_inv(float l) { return l == 0.f ? 0.f : 1.0f / l; }
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+}
+
 struct DecDesc {  // a row that starts in a CTA's piece and ends in a later one
   int b, hk, hb, slot, last_cta, pad[3];
 };
@@ -455,7 +465,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
           }
           m0 = fmaxf(m0, m[nt][0]);
           m1 = fmaxf(m1, m[nt][1]);
-          const float al0 = fast_exp2(m[nt][0] - m0), al1 = fast_exp2(m[nt][1] - m1);
+          const float al0 = fast_exp2(m[nt][0] - exp_base(m0)), al1 = fast_exp2(m[nt][1] - exp_base(m1));
           l[nt][0] *= al0;
           l[nt][1] *= al1;
 #pragma unroll
@@ -468,8 +478,9 @@ __global__ void __launch_bounds__(kDecWarps * 32)
           m[nt][0] = m0;
           m[nt][1] = m1;
         }
-        const float p0 = fast_exp2(x[0] - m[nt][0]), p1 = fast_exp2(x[1] - m[nt][1]);
-        const float p2 = fast_exp2(x[2] - m[nt][0]), p3 = fast_exp2(x[3] - m[nt][1]);
+        const float b0 = exp_base(m[nt][0]), b1 = exp_base(m[nt][1]);
+        const float p0 = fast_exp2(x[0] - b0), p1 = fast_exp2(x[1] - b1);
+        const float p2 = fast_exp2(x[2] - b0), p3 = fast_exp2(x[3] - b1);
         l[nt][0] += p0 + p2;
         l[nt][1] += p1 + p3;
         pb[nt][0] = transpose8x8(pack_bf16x2(p0, p1));  // keys along the product's inner side
@@ -529,7 +540,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       float mm = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, ml[(w * kHeads + h) * 2]);
-      const float base = mm == -INFINITY ? 0.f : mm;
+      const float base = exp_base(mm);
       float ll = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -544,11 +555,11 @@ __global__ void __launch_bounds__(kDecWarps * 32)
         o.w = fmaf(f, y.w, o.w);
       }
       if (whole) {
-        const float inv = ll > 0.f ? 1.0f / ll : 0.f;
+        const float inv = row_inv(ll);
         const size_t r = static_cast<size_t>(b) * g.Hq + h0 + h;
         *reinterpret_cast<uint2*>(out + r * D + d) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (d == 0) lse[r] = ll > 0.f ? (mm + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        if (d == 0) lse[r] = row_lse(mm, ll);
       } else {
         *reinterpret_cast<float4*>(pt + kHeads * 4 + h * D + d) = o;
         if (d == 0) *reinterpret_cast<float4*>(pt + h * 4) = make_float4(mm, ll, 0.f, 0.f);
@@ -615,7 +626,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, pm[k]);
-    const float base = bm == -INFINITY ? 0.f : bm, f0 = fast_exp2(mm - base);
+    const float base = exp_base(bm), f0 = fast_exp2(mm - base);
     mm = bm;
     ll *= f0;
 #pragma unroll
@@ -649,7 +660,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   mm = s_m[0];
 #pragma unroll
   for (int w = 1; w < kJoinWarps; ++w) mm = fmaxf(mm, s_m[w]);
-  const float base = mm == -INFINITY ? 0.f : mm;
+  const float base = exp_base(mm);
   float f[kJoinWarps];
   ll = 0.f;
 #pragma unroll
@@ -657,7 +668,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     f[w] = fast_exp2(s_m[w] - base);
     ll = fmaf(f[w], s_l[w], ll);
   }
-  const float inv = ll > 0.f ? 1.0f / ll : 0.f;
+  const float inv = row_inv(ll);
   const size_t r = static_cast<size_t>(d.b) * g.Hq + d.hk * g.G + d.hb * kHeads + h;
   for (int x = tid; x < D / 4; x += kJoinWarps * 32) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -672,7 +683,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     *reinterpret_cast<uint2*>(out + r * D + x * 4) =
         make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
   }
-  if (tid == 0) lse[r] = ll > 0.f ? (mm + __log2f(ll)) * 0.6931471805599453f : -INFINITY;
+  if (tid == 0) lse[r] = row_lse(mm, ll);
 }
 
 namespace {
