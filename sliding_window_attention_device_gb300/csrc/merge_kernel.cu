@@ -4,7 +4,8 @@
 //   lse = log(exp(lse_a) + exp(lse_b))
 //   out = exp(lse_a - lse) out_a + exp(lse_b - lse) out_b
 // A row whose two sides are both empty (lse = -inf) stays out = 0,
-// lse = -inf; an empty side has weight 0 whatever its out holds.
+// lse = -inf; an empty side has weight 0 whatever its out holds. A NaN on either
+// side stays one.
 //
 // Memory bound: each thread blends 8 bf16 values (16 bytes) of one row, two
 // such pieces for D = 512; the rows of a warp are whole (a row is at most one
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(256) merge_kernel(__nv_bfloat16* __restrict__ 
     __syncwarp();  // every lane has read its row's lse before it is rewritten
     const float m = fmaxf(la, lb);
     float wa = 0.f, wb = 0.f, l = -INFINITY;
-    if (m != -INFINITY) {
+    if (!(la == -INFINITY && lb == -INFINITY)) {  // (a NaN is no empty side)
       const float ea = expf(la - m), eb = expf(lb - m);  // an empty side gives exp(-inf) = 0
       const float tot = ea + eb;
       wa = ea / tot;
@@ -73,8 +74,8 @@ __global__ void __launch_bounds__(256) merge_kernel(__nv_bfloat16* __restrict__ 
           const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&av[e]);
           const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&bv[e]);
           // an empty side contributes nothing even if its values are not finite
-          const float lo = (wa > 0.f ? wa * __low2float(x) : 0.f) + (wb > 0.f ? wb * __low2float(y) : 0.f);
-          const float hi = (wa > 0.f ? wa * __high2float(x) : 0.f) + (wb > 0.f ? wb * __high2float(y) : 0.f);
+          const float lo = (wa != 0.f ? wa * __low2float(x) : 0.f) + (wb != 0.f ? wb * __low2float(y) : 0.f);
+          const float hi = (wa != 0.f ? wa * __high2float(x) : 0.f) + (wb != 0.f ? wb * __high2float(y) : 0.f);
           ov[e] = pack_bf16x2(lo, hi);
         }
         *reinterpret_cast<uint4*>(out + row * D + (part + u * kPerRow) * 8) = make_uint4(ov[0], ov[1], ov[2], ov[3]);
