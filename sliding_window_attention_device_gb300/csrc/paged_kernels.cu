@@ -238,8 +238,12 @@ __global__ void __launch_bounds__(kDecWarps * 32)
     b = blockIdx.x / rows_b;
     const int row = blockIdx.x % rows_b;
     const Visible v = visible_keys(g, seq_lens, b, &bad);
-    if (bad && tid == 0) atomicOr(status, BD_STATUS_BOUNDS);
-    if (*reinterpret_cast<const volatile int*>(status) != 0) return;
+    if (tid == 0) {  // read once: another CTA may set a bit between two threads' reads
+      if (bad) atomicOr(status, BD_STATUS_BOUNDS);
+      s_skip = *reinterpret_cast<const volatile int*>(status) != 0;
+    }
+    __syncthreads();
+    if (s_skip) return;
     const int steps = (v.n + kDecKeys - 1) / kDecKeys;
     if (steps == 0) {
       const int heads = min(kHeads, g.G - row % n_hb * kHeads);
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       if (lane >= o) incl += t;
     }
     if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
+    const bool any_bad = __syncthreads_or(bad) != 0;  // every CTA sees every length: then none writes
     long long total = 0, before = incl - mine;
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       total += s_sum[w];
     }
     if (tid == 0) desc[blockIdx.x].last_cta = -1;
-    if (s_skip) return;
+    if (s_skip || any_bad) return;
     // no fewer than one step per warp
     per = (total + gridDim.x - 1) / gridDim.x;
     if (per < kDecWarps) per = kDecWarps;
@@ -591,7 +595,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   constexpr int kBatch = D <= 128 ? 8 : D <= 256 ? 4 : 2;
   const int c0 = blockIdx.x / heads, h = blockIdx.x % heads;
   const DecDesc d = desc[c0];
-  if (*reinterpret_cast<const volatile int*>(status) != 0 || d.last_cta < 0 || h >= g.G - d.hb * kHeads) return;
+  if (d.last_cta < 0 || h >= g.G - d.hb * kHeads) return;
+  if (__syncthreads_or(*reinterpret_cast<const volatile int*>(status) != 0)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   __shared__ float4 s_o[kJoinWarps][D / 4];
