@@ -14,6 +14,9 @@
 // bytes: as few of both as the steps' order allows, and blocks no wider than the
 // row needs. K1 and K2 together 5.5 us at 256 positions, 8 at 2 x 4096, 12 at
 // 16384 (12, 22 and 26 with a block scan and a binary search per row and tile).
+// Ids that fall, 16384 rows in documents of 128: 25 us for 15 (91 with a scan and a
+// barrier per document); where only what is behind the shard falls, no more than
+// rising ones (131,072 positions, 16384 of them local: 38 us).
 //
 // K2 marks every (128-row q tile, 128-row K/V tile) as full, partial or empty.
 // A real row p may attend the keys [lo(p), p] with lo(p) = max(doc_start(p),
@@ -152,7 +155,8 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
 
   // One pass over the whole row: ids >= 0 and no document after padding; the
   // shard's first padding row (L if none); the start of the run that holds the
-  // shard's first position; whether ids ever fall from one document to the next.
+  // shard's first position; whether ids fall from one document to the next up to
+  // the shard's end.
   int flags = 0, first_pad = L, s_first = 0;  // flags: 1 bad layout, 2 falling ids
   {
     const int piece = cdiv(cdiv(g.S_full, 32), n_warps) * 32;
@@ -160,9 +164,9 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
 #pragma unroll 8
     for (int p = warp * piece + lane; p < e; p += 32) {
       const int c = row[p], prev = p > 0 ? row[p - 1] : c;
-      if (c < 0 || (c != 0 && prev == 0 && p > 0)) flags |= 1;
-      if (c != 0 && prev != 0 && c < prev) flags |= 2;
-      if (c == 0 && p >= ro && p < ro + L) first_pad = min(first_pad, p - ro);
+      if (c < 0 || (c != 0 && prev == 0)) flags |= 1;
+      if (c != 0 && c < prev && p < ro + L) flags |= 2;
+      if (c == 0 && p >= ro) first_pad = min(first_pad, p - ro);
       if (p <= ro && c != prev) s_first = p;
     }
   }
@@ -223,22 +227,35 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
   if (tid == 0) cu_q[n_seg] = n_real;
   __syncthreads();  // cu_q visible to the whole block
 
-  // Each local document id must not occur before its own run. Ids that never
-  // fall from one document to the next cannot; otherwise check every segment.
+  // Each local document id must not occur before its own run. Ids that never fall
+  // up to the shard's end cannot, nor ids that rise in the shard from one above
+  // every id before it; otherwise every run that starts before the shard's end is
+  // compared with the ids of the local segments that start behind it, a warp per
+  // run and no barrier between them.
   if (flags & 2) {
-    int dup = 0;
-    for (int k = 0; k < n_seg && !dup; ++k) {
-      const int idk = row[ro + cu_q[k]];
-      const int st = (k == 0) ? s_first : ro + cu_q[k];
-      int hit = 0;
-      for (int p = tid; p < st; p += nthr)
-        if (row[p] == idk) {
-          hit = 1;
-          break;
-        }
-      dup = __syncthreads_or(hit);
+    bool open = false;
+    if (n_seg > 0) {
+      const int id0 = row[ro];
+#pragma unroll 8
+      for (int p = tid; p < s_first; p += nthr) open |= row[p] >= id0;
+      for (int k = tid + 1; k < n_seg; k += nthr) open |= row[ro + cu_q[k]] <= row[ro + cu_q[k - 1]];
     }
-    bad |= dup;
+    if (!__syncthreads_or(open)) flags &= ~2;
+  }
+  if (flags & 2) {
+    bool hit = false;
+    const int e = ro + n_real;
+    for (int p0 = warp * 32; p0 < e; p0 += n_warps * 32) {
+      const int p = p0 + lane, c = p < e ? row[p] : 0;
+      unsigned m = __ballot_sync(0xffffffffu, p < e && (p == 0 || c != row[p - 1]));
+      for (; m; m &= m - 1) {
+        const int q = p0 + __ffs(m) - 1, id = __shfl_sync(0xffffffffu, c, __ffs(m) - 1);
+#pragma unroll 4
+        for (int k = lane; k < n_seg; k += 32)
+          hit |= q < (k == 0 ? s_first : ro + cu_q[k]) && row[ro + cu_q[k]] == id;
+      }
+    }
+    bad |= __syncthreads_or(hit);
   }
 
   // cu_k and the maxima.
