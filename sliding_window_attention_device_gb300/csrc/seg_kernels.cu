@@ -573,9 +573,10 @@ cudaError_t launch_seg_build(const int32_t* doc, const Geom& g, int32_t* seg, in
       le != cudaSuccess) return le;
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // histogram bins of the work-list sort (48 KB of shared memory at most)
+  // histogram bins of the work-list sort: 48 KB of shared memory at most, the
+  // kernel's static words included (longer items share the last bin)
   int nbins = (g.nkt > cdiv(g.L, kBwdQ) ? g.nkt : cdiv(g.L, kBwdQ)) + 1;
-  if (nbins > 12288) nbins = 12288;
+  if (nbins > 12288 - 64) nbins = 12288 - 64;
   const int widest = g.nkt > g.nqt ? g.nkt : g.nqt;
   if (const cudaError_t le = launch_pdl(classify_kernel, dim3(g.sink_tab ? 3 : 2),
                                         threads(static_cast<long long>(g.B) * widest),
