@@ -113,6 +113,10 @@ int to_geom(const bd_geom* in, Geom* g) {
   if (in->S_full > (1 << 28) || static_cast<long long>(in->B) * in->Hq > (1 << 20)) return BD_ERR_ARG;
   if (static_cast<long long>(in->B) * (in->L + 1) * 4 + static_cast<long long>(in->B) * in->S_kv > (1LL << 29))
     return BD_ERR_ARG;
+  // and the table's words (the tile bitmap grows with L * S_kv)
+  const long long nqt = cdiv(in->L, kTile), nkt = cdiv(in->S_kv, kTile);
+  if (in->B * (BD_SEG_HDR_WORDS + 3LL * (in->L + 1) + 3 * nqt + 3 * nkt + nqt * ((nkt + 31) / 32)) > 0x7fffffffLL - 64)
+    return BD_ERR_ARG;
   if (!(in->scale == in->scale)) return BD_ERR_ARG;  // NaN
   if (in->kv_layout != BD_KV_BHSD && in->kv_layout != BD_KV_SBHD) return BD_ERR_ARG;
   if (!(in->dropout_p >= 0.f && in->dropout_p < 1.f)) return BD_ERR_ARG;  // also NaN
