@@ -256,9 +256,9 @@ __device__ __forceinline__ uint32_t keep_bits32(const uint32_t (&km)[4], int c0)
 // and sk_rows alike and the counts within capacity the units say the rest.
 __device__ __forceinline__ int sink_n_units(const Geom& g, const int32_t* seg) {
   const int32_t* hdr = seg + g.off[BD_SEG_OFF_HDR];
-  const int4 cut = *reinterpret_cast<const int4*>(hdr + kHdrSinkCut);
-  if (!seg_hdr_ok(g, hdr) || hdr[kHdrSinkTab] != 1 || cut.x != g.B || cut.y != g.G || cut.z != g.sk_units ||
-      cut.w != g.sk_rows)
+  const int4 cut = *reinterpret_cast<const int4*>(hdr + kHdrSinkCut);  // one trip with the header's other words
+  if (!(seg_hdr_ok(g, hdr) & (hdr[kHdrSinkTab] == 1) & (cut.x == g.B) & (cut.y == g.G) & (cut.z == g.sk_units) &
+        (cut.w == g.sk_rows)))
     return -1;
   const int4 n = *reinterpret_cast<const int4*>(seg + g.sk_off);
   return n.x <= g.sk_units && n.y <= g.sk_sums && n.z <= g.sk_slots ? n.x : -1;
