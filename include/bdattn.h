@@ -36,6 +36,8 @@
  * gemma4_moe.cp_attention). All device pointers are caller-owned and must be
  * 16-byte aligned. The library allocates no device memory and never
  * synchronises the stream; every entry point only enqueues work on `stream`.
+ * Grids and cuts of the work are sized for the 152 SMs of a GB300; on a part with
+ * fewer the results are right and a split call may take a second wave of CTAs.
  *
  * Errors:
  *   - return value: BD_OK, or an argument / CUDA error found on the host

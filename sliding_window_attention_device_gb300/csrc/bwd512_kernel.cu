@@ -29,6 +29,7 @@
 // With attention dropout (kDrop) each P / dS warp draws its 32 keys' keep
 // masks over the half's q columns (dropout.cuh): dropped weights are zeroed in
 // P^T, dS = P (Z dP - delta), and dV is scaled by the keep scale when written.
+// P^T and dS^T are rounded to bf16 for their products; every sum is fp32.
 // With sinks (kSink) a CTA's work is a slice of a unit of a sink table
 // (common.cuh): a K/V tile, some of its q rows, some or all of the group's heads.
 #include <cuda.h>

@@ -18,6 +18,7 @@
 //   warp 2  tensor memory       warps 4-7  softmax, thread = q row
 // The softmax is K3's: online max / sum in fp32, the mask only on tiles a row
 // sees partly, O rescaled only when the running max grows by more than 2^8.
+// P is rounded to bf16 for the product (the row sum is of the unrounded P, in fp32).
 // With attention dropout (kDrop) each row draws its keep mask of a tile before
 // the tile's S arrives and zeroes the dropped weights of P; the keep scale is
 // folded into the final normalisation.

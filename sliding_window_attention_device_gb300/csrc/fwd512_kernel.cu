@@ -15,6 +15,7 @@
 //            a V half per tile
 //   warp 1   one thread issues the MMAs      warp 2  tensor memory
 //   warps 4-7  thread = q row: softmax, P (bf16 over S in tensor memory), out
+// P is rounded to bf16 for the product (the row sum is of the unrounded P, in fp32).
 // With attention dropout (kDrop) each row draws its keep mask of a tile (in
 // both passes) before the tile's S arrives, zeroes the dropped weights of the
 // P it hands to the PV products (the row sum stays the undropped one) and

@@ -32,8 +32,9 @@ constexpr int kDecWarps = 4;
 constexpr int kDecKeys = 16;
 __host__ __device__ inline int dec_ctas(int D) { return D <= 256 ? 2 * kSms : kSms; }
 __host__ __device__ inline int dec_head_tiles(int D, int G) { return D <= 256 && G > 8 ? 2 : 1; }
-// Whether a CTA takes whole rows: no sequence can show a new token many keys,
-// or not very many and there are rows for most SMs.
+// Whether a CTA takes whole rows, by the most keys that the table's capacity and
+// the window let a new token see (the lengths are on the device): few, or not
+// very many and there are rows for most SMs.
 __host__ __device__ inline bool dec_whole_rows(const PagedGeom& g) {
   long long n = static_cast<long long>(g.max_pages) * g.page_size;
   if (g.window > 0 && n > static_cast<long long>(g.window) + g.n_sink) n = static_cast<long long>(g.window) + g.n_sink;

@@ -19,7 +19,8 @@ namespace bd {
 // sequence (binary search in cu_new), page and cache row, then all copy
 // 16-byte pieces, K and V together. Reads and writes every new element once: the
 // bytes bound it. 19,200 tokens of 12 prompts (8 kv heads, D 128, 157 MB in all),
-// new data each time: 27 us, 5.8 TB/s; 64 single tokens 3 us, a launch's cost.
+// new data each time: 27 us, 5.8 TB/s; 64 single tokens 3 us, a launch's cost. The
+// offsets' check (CTA 0, and each token's own range) costs nothing beside these.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTok = 16;
 
@@ -105,8 +106,10 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int3
 
 // ------------------------------------------------------------------ decode
 // out = softmax(scale q K^T) V of one query row per head over the sequence's
-// visible keys. Every K and V row is read once and used by the G query heads of
-// its kv head: G FLOPs a byte, so the cache's bytes bound it, not the products.
+// visible keys. A K or V row is read once for up to 16 query heads of its kv head
+// (8 at D 512), so the cache's bytes bound it, not the products. A larger group
+// reads the cache again for each such block: 16 sequences of 8,000 keys, 4 kv
+// heads, D 128: G 8 39 us, 16 46, 32 74, 64 132.
 //
 // A (sequence, kv head, block of up to 16 query heads) is a row of work; its
 // visible keys, sinks first, then the window, are numbered without a gap and cut
@@ -125,7 +128,11 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int3
 //   over a tensor where its own rounding is 0.0017; at most 6% more time where a
 //   CTA's chain is all there is (8 x 500 keys 8.0 -> 8.5 us), else within 3%.
 // Where sequences are short, or not long and rows many (dec_whole_rows), a CTA
-// takes a whole row instead: no line, no second kernel. At 1,028 visible keys
+// takes a whole row instead: no line, no second kernel. The host decides it, and
+// knows the table's capacity and the window but not the lengths: short sequences
+// under a large table take the cut line (100 keys, D 64, alone 7.8 us for 4.1;
+// 8 kv heads, D 128, 64 x 100 keys 13.0 for 8.6, 64 x 500 22.4 for 19.1). At 1,028
+// visible keys
 // (window 1024) and 8 kv heads, D 128: 16 sequences 14.6 us whole, 16.4 cut; 64
 // 42.5 and 56.3; but 4 sequences 14.0 and 11.1. At 4,100 keys about even, and cut
 // pieces are the safer choice for ragged lengths.
@@ -134,8 +141,8 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int3
 // score passes it by 2^8 (one vote instead of three rounds of shuffles), and a
 // page id is loaded a step before it is used (D 64, whole rows of 4,100 keys: 48
 // -> 34 us). With all SMs at work the cache's bytes bound it: 16 ragged sequences
-// up to 32,768 keys, 8 kv heads, D 128, 1.06 GB in 170 us, 6.2 TB/s; one sequence
-// of 131,072 keys, 4 kv heads, 268 MB in 52 us (7 us of these start and join).
+// up to 32,768 keys, 8 kv heads, D 128, 1.06 GB in 172 us, 6.2 TB/s; one sequence
+// of 131,072 keys, 4 kv heads, 268 MB in 51 us (7 us of these start and join).
 // Rings of 4 items or 6, 2 or 3 CTAs an SM, 4 or 8 warps a CTA: within 3%.
 // At the end of a row's piece the warps join through shared memory. A row
 // inside one CTA is written at once; of a row cut over CTAs each leaves (m, l,
