@@ -75,6 +75,22 @@ class Paged(ctypes.Structure):
 KV_BHSD, KV_SBHD = 0, 1  # K/V layouts: [B, Hkv, S_kv, D] or token-major [S_kv, B, Hkv, D]
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _fit(struct, values):
+    """Refuses what does not fit the struct's C ints, which ctypes would wrap."""
+    if max(values) > _INT_MAX or min(values) < -_INT_MAX:
+        for (name, _), x in zip(struct._fields_, values):
+            if not -_INT_MAX <= x <= _INT_MAX:
+                raise ValueError(f"{name}={x} does not fit 32 bits")
+
+
+def _c_window(window) -> int:
+    """Beyond every distance, or none."""
+    return _INT_MAX if window > _INT_MAX else -1 if window < 0 else int(window)
+
+
 def geom(B, Hq, Hkv, D, S_full, L, row_offset, kv_offset, S_kv, window=0, scale=0.0, kv_layout=KV_BHSD,
          dropout_p=0.0, seed=0) -> Geom:
     """Geometry of one query shard: local rows [row_offset, row_offset+L) of a
@@ -84,8 +100,9 @@ def geom(B, Hq, Hkv, D, S_full, L, row_offset, kv_offset, S_kv, window=0, scale=
     attention dropout drawn from the 64-bit `seed` (the same p and seed in the
     forward and the backward of a step)."""
     seed = int(seed) & 0xFFFFFFFFFFFFFFFF
-    return Geom(int(B), int(Hq), int(Hkv), int(D), int(S_full), int(L), int(row_offset), int(kv_offset),
-                int(S_kv), int(window), float(scale or 0.0), int(kv_layout), float(dropout_p), seed & 0xFFFFFFFF,
+    v = (int(B), int(Hq), int(Hkv), int(D), int(S_full), int(L), int(row_offset), int(kv_offset), int(S_kv))
+    _fit(Geom, v)
+    return Geom(*v, _c_window(window), float(scale or 0.0), int(kv_layout), float(dropout_p), seed & 0xFFFFFFFF,
                 seed >> 32)
 
 
@@ -507,14 +524,14 @@ _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def sink_seg_bytes(g: Geom, n_sink: int) -> int:
-    n = load().bd_attn_sink_seg_bytes(ctypes.byref(g), int(n_sink))
+    n = load().bd_attn_sink_seg_bytes(ctypes.byref(g), int(n_sink)) if 0 <= n_sink <= SINK_MAX else 0
     if n == 0:
         raise ValueError(f"invalid geometry {g} or n_sink={n_sink} (0 to {SINK_MAX})")
     return int(n)
 
 
 def sink_bwd_workspace_bytes(g: Geom, n_sink: int) -> int:
-    n = load().bd_attn_sink_bwd_workspace_bytes(ctypes.byref(g), int(n_sink))
+    n = load().bd_attn_sink_bwd_workspace_bytes(ctypes.byref(g), int(n_sink)) if 0 <= n_sink <= SINK_MAX else 0
     if n == 0:
         raise ValueError(f"invalid geometry {g} or n_sink={n_sink} (0 to {SINK_MAX})")
     return int(n)
@@ -637,8 +654,10 @@ def paged_geom(B, Hq, Hkv, D, n_pages, page_size, max_pages, window=0, n_sink=0,
     """Geometry of a paged cache [n_pages, Hkv, page_size, D] and the B sequences
     in it (page table [B, max_pages]); window <= 0: none; n_sink: first tokens
     that stay visible past the window; scale <= 0 means D**-0.5."""
-    return Paged(int(B), int(Hq), int(Hkv), int(D), int(n_pages), int(page_size), int(max_pages), int(window),
-                 int(n_sink), float(scale or 0.0))
+    v = (int(B), int(Hq), int(Hkv), int(D), int(n_pages), int(page_size), int(max_pages), _c_window(window),
+         int(n_sink) if n_sink <= _INT_MAX else _INT_MAX)
+    _fit(Paged, v)
+    return Paged(*v, float(scale or 0.0))
 
 
 def paged_decode_workspace_bytes(pg: Paged) -> int:
