@@ -250,10 +250,19 @@ __global__ void __launch_bounds__(1024) seg_build_kernel(const int32_t* __restri
     for (int p0 = warp * 32; p0 < e; p0 += n_warps * 32) {
       const int p = p0 + lane, c = p < e ? row[p] : 0;
       unsigned m = __ballot_sync(0xffffffffu, p < e && (p == 0 || c != row[p - 1]));
+      if (m == 0) continue;
+      // With many segments from the first one on that does not start before these 32
+      // positions (finding it is a chain of loads: with 128 segments 34 us for 25, with
+      // 4096 890 for 1,615).
+      int k0 = 0, k1 = n_seg > 512 ? n_seg : 0;
+      while (k0 < k1) {
+        const int mid = (k0 + k1) >> 1;
+        if ((mid == 0 ? s_first : ro + cu_q[mid]) < p0) k0 = mid + 1; else k1 = mid;
+      }
       for (; m; m &= m - 1) {
         const int q = p0 + __ffs(m) - 1, id = __shfl_sync(0xffffffffu, c, __ffs(m) - 1);
 #pragma unroll 4
-        for (int k = lane; k < n_seg; k += 32)
+        for (int k = k0 + lane; k < n_seg; k += 32)
           hit |= q < (k == 0 ? s_first : ro + cu_q[k]) && row[ro + cu_q[k]] == id;
       }
     }

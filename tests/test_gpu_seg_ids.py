@@ -67,7 +67,7 @@ def rows(rng, B, S, ro, L, mean, kind):
 
 KINDS = ["rising", "falling", "any_order", "restart_behind", "falling_before", "few", "one_repeat"]
 SHAPES = [(300, 0, 300, 1), (300, 100, 90, 3), (513, 128, 257, 20), (1000, 999, 1, 40), (1000, 0, 1, 40),
-          (4000, 1300, 1500, 60), (70, 33, 37, 2)]
+          (4000, 1300, 1500, 60), (70, 33, 37, 2), (3000, 400, 2000, 1)]  # (the last: more than 512 segments)
 
 
 @pytest.mark.parametrize("kind", KINDS)
