@@ -124,18 +124,17 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int3
 //   tensor rate is not what bounds this: one mma covers 512 bytes of cache.)
 //   Softmax statistics and O in fp32. P enters the product as two bf16 numbers,
 //   the second of what the first left (off by 2^-16): a second mma on the same V
-//   fragments, which the bytes hide. With one, out was off by 0.0020 to 0.0024
-//   over a tensor where its own rounding is 0.0017; at most 6% more time where a
-//   CTA's chain is all there is (8 x 500 keys 8.0 -> 8.5 us), else within 3%.
+//   fragments, which the bytes hide. With one number, out is off by 0.0020 to 0.0024
+//   over a tensor where its own rounding is 0.0017; at most 6% less time where a
+//   CTA's chain is all there is (8 x 500 keys 8.0 us for 8.5), else within 3%.
 // Where sequences are short, or not long and rows many (dec_whole_rows), a CTA
 // takes a whole row instead: no line, no second kernel. The host decides it, and
 // knows the table's capacity and the window but not the lengths: short sequences
 // under a large table take the cut line (100 keys, D 64, alone 7.8 us for 4.1;
 // 8 kv heads, D 128, 64 x 100 keys 13.0 for 8.6, 64 x 500 22.4 for 19.1). At 1,028
-// visible keys
-// (window 1024) and 8 kv heads, D 128: 16 sequences 14.6 us whole, 16.4 cut; 64
-// 42.5 and 56.3; but 4 sequences 14.0 and 11.1. At 4,100 keys about even, and cut
-// pieces are the safer choice for ragged lengths.
+// visible keys (window 1024) and 8 kv heads, D 128: 16 sequences 14.6 us whole, 16.4
+// cut; 64 42.5 and 56.3; but 4 sequences 14.0 and 11.1. At 4,100 keys about even, and
+// cut pieces are the safer choice for ragged lengths.
 // A step's chain (scores, maximum, exponentials, P V) is what bounds a CTA alone:
 // so the score products run in four chains, the maximum is raised only when a
 // score passes it by 2^8 (one vote instead of three rounds of shuffles), and a
