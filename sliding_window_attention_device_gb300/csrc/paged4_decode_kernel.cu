@@ -8,8 +8,14 @@
 // bits and lies between 2^-10 and 2688: exact in fp16. So the products are fp16 mma.sync
 // m16n8k16 with fp32 sums; q, whose range fp16 lacks, is scaled by a power of two per
 // head that its scores are multiplied with afterwards; P is taken against the maximum
-// less 7 (in log2), up to 2^15, so that fp16's smallest step is 2^-32 of the largest
-// weight, and one fp16 number per weight (off by 2^-11) is enough.
+// less 7 (in log2), so the largest weight is between 2^7 and 2^15 and fp16's smallest
+// step, 2^-24, is at most 2^-31 of it; and each weight is two fp16 numbers, the second of
+// what the first left, off by 2^-22 of it or by 2^-32 of the largest: out is then off by
+// its own rounding only. The second one costs a second product with V, but where a row
+// has at most 4 heads (kFold): they stand twice among a product's 8 columns, which hold
+// first parts in one half and second parts in the other. Two products: 16 sequences to
+// 32,768 keys at 8 heads 75 us (one number per weight: 67), at 16 heads 110 (92); folded:
+// 32 sequences with a window of 1024 at D 256 and 2 heads 22.5 (22.1).
 //   The order of d within a product and of keys within a step is free as long as both
 // factors share it. So lane (g, c) = (lane / 4, lane % 4) of the K product reads a
 // quarter of a key's row, D / 8 bytes, from shared memory at once and makes its part of
@@ -26,15 +32,17 @@
 // goes from one row to the next waits for a page number, for keys and for its warps.
 //
 // What bounds it. 16 keys of D 128 are 2,304 bytes, 392 clocks of an SM's quarter at the
-// copy rate, and 304 instructions (measured; 64 conversions, 64 products with scales,
-// 16 mma, 12 loads from shared memory, the rest copies, softmax and addresses). Without
-// any copies the same work takes 327 clocks: conversions, half-precision products and
-// mma.sync hardly overlap on the SM. So instructions and bytes bound it about alike. 16
-// ragged sequences to 32,768 keys, 8 kv heads, D 128, 312 MB: 67 us, 4.7 TB/s (the bf16
-// pages of the same keys: 172 us); D 64, 156 MB 45 us; D 256, 313 MB 69; D 512 64. A call
-// with few steps is 3 us of a launch, page number, keys and softmax, one after the other,
-// and 2 to 3 of the join: one sequence of 1,000 keys 8 us, of 131,072 (75 MB) 24.
-//   Tried and not kept, for the 312 MB: bulk copies by one lane 79 us for 67 (many small
+// copy rate, and some 320 instructions (304 measured with one number per weight: 64
+// conversions, 64 products with scales, 16 mma, 12 loads from shared memory, the rest
+// copies, softmax and addresses; the second one adds 8 mma and a dozen more). Without any
+// copies that took 327 clocks, and 8 mma are some 65: conversions, half-precision
+// products and mma.sync hardly overlap on the SM. So instructions bound it, bytes close
+// behind. 16 ragged sequences to 32,768 keys, 8 kv heads of 8 heads each, D 128, 312 MB:
+// 75 us, 4.2 TB/s (the bf16 pages of the same keys: 172 us); D 64, 156 MB 50 us; D 256,
+// 313 MB 76; D 512 68. With 16 heads each D 64 72, D 128 110, D 256 109. A call with few
+// steps is 3 us of a launch, page number, keys and softmax, one after the other, and 2 to
+// 3 of the join: one sequence of 1,000 keys 8 us, of 131,072 (75 MB) 26.
+//   Tried and not kept, for the 312 MB, all with one number per weight: bulk copies by one lane 79 us for 67 (many small
 // ones); K and V as items of their own 77 for 74; 24 warps an SM at 80 registers 105;
 // every warp with a piece of the line of its own 69 for 72, but 28 for 22 at 1,028 keys
 // of D 256. Two CTAs an SM, but for 16 heads at D 128 (91 us with one and 236 registers,
@@ -214,7 +222,7 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t top, uint32_t pair) {
   return max(top, max((pair << 16) & 0x7fffffffu, pair & 0x7fff0000u));
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kFold>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     paged4_decode_kernel(const __nv_bfloat16* __restrict__ q, const Cache4 c4, const int32_t* __restrict__ page_table,
                          const int32_t* __restrict__ seq_lens, const PagedGeom g, int mode,
@@ -222,7 +230,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                          float* __restrict__ part, int32_t* status) {
   pdl_begin();
   using C = Cfg<D, NT>;
+  static_assert(!kFold || NT == 1, "");
   constexpr int kHeads = C::kHeads, kKs = D / 16;
+  constexpr int kParts = kFold ? 1 : 2;  // columns that P's two parts take of their own
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_sum[kWarps];
   __shared__ int s_b, s_skip;
@@ -427,20 +437,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
       for (int y = 0; y < kQHeads; ++y) {
         const int h = C::kQSmem ? warp + y * kWarps : y * 8 + gr;
-        const bool has = h < heads;
+        const int hq = kFold ? h & 3 : h;  // folded: heads 0 to 3 once more in columns 4 to 7
+        const bool has = hq < heads;
         if constexpr (C::kQSmem) {
 #pragma unroll
           for (int x = 0; x < kQLoads; ++x) {
             const int i = x * 32 + lane;  // (ks, c)
             uint2 u = make_uint2(0u, 0u);
-            if (has) u = *reinterpret_cast<const uint2*>(qb + h * D + (i & 3) * (D / 4) + 4 * (i >> 2));
+            if (has) u = *reinterpret_cast<const uint2*>(qb + hq * D + (i & 3) * (D / 4) + 4 * (i >> 2));
             qf[y][x][0] = u.x, qf[y][x][1] = u.y;
           }
         } else {
 #pragma unroll
           for (int ks = 0; ks < kKs; ks += 2) {
             uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (has) u = *reinterpret_cast<const uint4*>(qb + h * D + cl * (D / 4) + 4 * ks);
+            if (has) u = *reinterpret_cast<const uint4*>(qb + hq * D + cl * (D / 4) + 4 * ks);
             qf[y][ks][0] = u.x, qf[y][ks][1] = u.y, qf[y][ks + 1][0] = u.z, qf[y][ks + 1][1] = u.w;
           }
         }
@@ -704,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
             limit[nt][h] = now + kRaise;
           }
       }
-      uint32_t pb[kGroups][NT][2];
+      // P in two fp16 parts, the second of what the first left; folded, columns 4 to 7 hold the second ones
+      uint32_t pb[kGroups][NT][kParts][2];
 #pragma unroll
       for (int q = 0; q < kGroups; ++q)
 #pragma unroll
@@ -714,8 +726,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           for (int y = 0; y < 4; ++y) p[y] = fast_exp2(fmaf(x[q][nt][y], back[nt][y & 1], neg_base[nt][y & 1]));
           l[nt][0] += p[0] + p[2];
           l[nt][1] += p[1] + p[3];
-          pb[q][nt][0] = transpose8x8(pack_half2(p[0], p[1]));  // keys along the product's inner side
-          pb[q][nt][1] = transpose8x8(pack_half2(p[2], p[3]));
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {  // keys along the product's inner side
+            const uint32_t first = pack_half2(p[2 * z], p[2 * z + 1]);
+            const float2 f = floats_of(first);
+            const uint32_t second = pack_half2(p[2 * z] - f.x, p[2 * z + 1] - f.y);
+            if constexpr (kFold) {
+              pb[q][nt][0][z] = transpose8x8(cl < 2 ? first : second);
+            } else {
+              pb[q][nt][0][z] = transpose8x8(first);
+              pb[q][nt][kParts - 1][z] = transpose8x8(second);
+            }
+          }
         }
       // ---- O^T += V^T P^T: rows g and g + 8 of product j are d = g D / 8 + 2 j and + 1
 #pragma unroll
@@ -745,7 +767,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           for (int e = 0; e < 4; ++e) {
             const uint32_t a[4] = {mul_h2(v[0][e], f0), mul_h2(v[1][e], f0), mul_h2(v[2][e], f1), mul_h2(v[3][e], f1)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][4 * y + e], a, pb[q][nt][0], pb[q][nt][1]);
+            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(acc[nt][4 * y + e], a, pb[q][nt][part][0], pb[q][nt][part][1]);
           }
         }
       }
@@ -793,12 +818,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       for (int w = 0; w < kWarps; ++w) {
         const float f = fast_exp2(ml[(w * kHeads + h) * 2] - base);
         ll += f * ml[(w * kHeads + h) * 2 + 1];
-        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(
-                                                              smem + w * C::kItems * C::kItem) + h * C::kOStride + d);
-        o.x = fmaf(f, y.x, o.x);
-        o.y = fmaf(f, y.y, o.y);
-        o.z = fmaf(f, y.z, o.z);
-        o.w = fmaf(f, y.w, o.w);
+        auto add = [&](float f, int column) {
+          const float4 y = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(smem + w * C::kItems * C::kItem) + column * C::kOStride + d);
+          o.x = fmaf(f, y.x, o.x);
+          o.y = fmaf(f, y.y, o.y);
+          o.z = fmaf(f, y.z, o.z);
+          o.w = fmaf(f, y.w, o.w);
+        };
+        add(f, h);
+        if constexpr (kFold) add(fast_exp2(ml[(w * kHeads + h + 4) * 2] - base), h + 4);
       }
       o.x *= c4.v_gain, o.y *= c4.v_gain, o.z *= c4.v_gain, o.w *= c4.v_gain;
       if (whole) {
@@ -837,11 +866,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kFold = false>
 cudaError_t launch_dn(const void* q, const Cache4& c4, const int32_t* page_table, const int32_t* seq_lens,
                       const PagedGeom& g, void* out, float* lse, void* workspace, int32_t* status, cudaStream_t st) {
   using C = Cfg<D, NT>;
-  auto kern = paged4_decode_kernel<D, NT>;
+  auto kern = paged4_decode_kernel<D, NT, kFold>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   DecDesc* desc = static_cast<DecDesc*>(workspace);
@@ -874,13 +903,13 @@ size_t paged4_decode_workspace_bytes(const PagedGeom& g) {
 cudaError_t launch_paged4_decode(const void* q, const Cache4& c4, const int32_t* page_table, const int32_t* seq_lens,
                                  const PagedGeom& g, void* out, float* lse, void* workspace, int32_t* status,
                                  cudaStream_t st) {
-  const bool two = dec_head_tiles(g.D, g.G) == 2;
-#define BD_DECODE4(D, NT) launch_dn<D, NT>(q, c4, page_table, seq_lens, g, out, lse, workspace, status, st)
+  const bool two = dec_head_tiles(g.D, g.G) == 2, fold = g.G <= 4;
+#define BD_DECODE4(...) launch_dn<__VA_ARGS__>(q, c4, page_table, seq_lens, g, out, lse, workspace, status, st)
   switch (g.D) {
-    case 64: return two ? BD_DECODE4(64, 2) : BD_DECODE4(64, 1);
-    case 128: return two ? BD_DECODE4(128, 2) : BD_DECODE4(128, 1);
-    case 256: return two ? BD_DECODE4(256, 2) : BD_DECODE4(256, 1);
-    case 512: return BD_DECODE4(512, 1);
+    case 64: return two ? BD_DECODE4(64, 2) : fold ? BD_DECODE4(64, 1, true) : BD_DECODE4(64, 1);
+    case 128: return two ? BD_DECODE4(128, 2) : fold ? BD_DECODE4(128, 1, true) : BD_DECODE4(128, 1);
+    case 256: return two ? BD_DECODE4(256, 2) : fold ? BD_DECODE4(256, 1, true) : BD_DECODE4(256, 1);
+    case 512: return fold ? BD_DECODE4(512, 1, true) : BD_DECODE4(512, 1);
     default: return cudaErrorInvalidValue;
   }
 #undef BD_DECODE4
