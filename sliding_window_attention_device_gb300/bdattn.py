@@ -3,8 +3,9 @@
 Argument marshalling only: every computation runs in the CUDA kernels behind
 the C ABI. Tensors are PyTorch CUDA tensors (PyTorch provides the device
 memory and the current stream); outputs the caller does not pass are
-allocated here with torch. Small calls of the paged operators go through _calls, a
-module built with the library, which does the same. There is no CPU fallback: without the compiled
+allocated here with torch. Small calls of the rotating append and the 4-bit cache go
+through _calls, a module built with the library, which does the same and without which
+they go through the functions here. There is no CPU fallback: without the compiled
 library, or without a GPU, these functions raise.
 """
 from __future__ import annotations
@@ -12,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 from typing import NamedTuple
 
 import torch
@@ -141,6 +143,19 @@ _lib = None
 _calls = None  # the module behind which small calls are made without Python (csrc/calls.cpp)
 
 
+def _native_calls():
+    """The module _calls, or None, with a warning, where it cannot be loaded: no operator needs it."""
+    try:
+        from . import _calls as calls
+    except ImportError as e:
+        warnings.warn(f"_calls cannot be loaded ({e}): small calls of the paged operators take some 10 us more of the "
+                      "host's time; `python -m sliding_window_attention_device_gb300.build` builds it",
+                      RuntimeWarning, stacklevel=3)
+        return None
+    calls.setup(Paged)
+    return calls
+
+
 def load() -> ctypes.CDLL:
     """Load libbdattn.so (raises if it has not been built)."""
     global _lib, _calls
@@ -224,9 +239,7 @@ def load() -> ctypes.CDLL:
         lib.bd_attn_paged4_decode_workspace_bytes.restype = ctypes.c_size_t
         lib.bd_attn_paged4_decode.argtypes = [P, C4, P, P, PG, P, P, P, P, P]
         lib.bd_attn_paged4_decode.restype = I
-        from . import _calls as calls
-        calls.setup(Paged)
-        _calls = calls
+        _calls = _native_calls()
         lib.bd_attn_strerror.argtypes = [ctypes.c_int]
         lib.bd_attn_strerror.restype = ctypes.c_char_p
         lib.bd_attn_selftest_wait_timeout.argtypes = [P, ctypes.c_uint64, P]

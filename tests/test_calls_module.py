@@ -1,0 +1,58 @@
+"""The binding's native part is an addition: without it every operator still runs, through Python and the C ABI."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from sliding_window_attention_device_gb300 import build
+
+PKG = os.path.dirname(build.__file__)
+
+
+@pytest.fixture(scope="module")
+def built():
+    build.build()
+
+
+def package_in(folder, leave_out=lambda name: name.startswith("_calls")):
+    """The package's Python files and libraries in another folder, some left out."""
+    to = folder / os.path.basename(PKG)
+    to.mkdir()
+    for name in os.listdir(PKG):
+        if name.endswith((".py", ".so")) and not leave_out(name):
+            (to / name).symlink_to(os.path.join(PKG, name))
+    return folder
+
+
+def python(folder, code):
+    head = f"import sys; sys.path.insert(0, {str(folder)!r})\nfrom sliding_window_attention_device_gb300 import bdattn\n"
+    env = {k: v for k, v in os.environ.items() if k != "PYTHONPATH"}
+    return subprocess.run([sys.executable, "-c", head + code], capture_output=True, text=True, cwd=folder, env=env)
+
+
+def test_without_the_native_calls(built, tmp_path):
+    """A package that holds the library alone loads, answers, and says what is slower."""
+    r = python(package_in(tmp_path), f"""
+assert bdattn.__file__.startswith({str(tmp_path)!r})
+lib = bdattn.load()
+assert bdattn._calls is None
+pg = bdattn.paged_geom(4, 8, 2, 128, 100, 16, 200)
+assert bdattn.paged4_decode_workspace_bytes(pg) > 0 and bdattn.paged_decode_workspace_bytes(pg) > 0
+g = bdattn.geom(1, 2, 1, 64, 256, 64, 0, 0, 256)
+assert bdattn.seg_bytes(g) > 0
+for call in (bdattn.bd_attn_paged4_decode, bdattn.bd_attn_paged_decode):
+    try:
+        call(*[None] * (6 if "4" in call.__name__ else 7))
+    except ValueError as e:
+        assert "CUDA tensor" in str(e)
+    else:
+        raise AssertionError
+""")
+    assert r.returncode == 0, r.stderr
+    assert r.stderr.count("RuntimeWarning") == 1 and "_calls" in r.stderr
+
+
+def test_with_them(built, tmp_path):
+    r = python(package_in(tmp_path, lambda name: False), "bdattn.load()\nassert bdattn._calls is not None")
+    assert r.returncode == 0 and "Warning" not in r.stderr, r.stderr
