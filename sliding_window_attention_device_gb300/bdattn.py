@@ -11,12 +11,15 @@ library, or without a GPU, these functions raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 import warnings
 from typing import NamedTuple
 
 import torch
+
+from .build import calls_path
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbdattn.so")
@@ -144,9 +147,12 @@ _calls = None  # the module behind which small calls are made without Python (cs
 
 
 def _native_calls():
-    """The module _calls, or None, with a warning, where it cannot be loaded: no operator needs it."""
+    """The module _calls of this torch and Python, or None, with a warning, where it cannot be loaded: no operator
+    needs it."""
     try:
-        from . import _calls as calls
+        spec = importlib.util.spec_from_file_location(f"{__package__}._calls", calls_path())
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
     except ImportError as e:
         warnings.warn(f"_calls cannot be loaded ({e}): small calls of the paged operators take some 10 us more of the "
                       "host's time; `python -m sliding_window_attention_device_gb300.build` builds it",

@@ -1,9 +1,9 @@
 """Builds libbdattn.so (the CUDA kernels behind include/bdattn.h) in-tree with nvcc.
 
 Every translation unit is compiled for sm_103a only, in parallel, then linked
-into one shared library next to this file; so is _calls.so, the part of the
-Python binding that small calls go through (g++, against the Python and torch
-that are installed). Run as ``python -m
+into one shared library next to this file; so is _calls, the part of the Python
+binding that small calls go through (g++, against the Python and torch that are
+installed, of which its file is named). Run as ``python -m
 sliding_window_attention_device_gb300.build``.
 """
 from __future__ import annotations
@@ -12,6 +12,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -22,7 +23,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbdattn.so")
-CALLS = os.path.join(PKG, "_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{os.path.join(ROOT, 'include')}"]
 
@@ -46,11 +46,24 @@ def _calls_source() -> str:
     return os.path.join(CSRC, "calls.cpp")
 
 
-def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return any(os.path.getmtime(p) > t for p in _sources() + _headers() + [_calls_source(), __file__])
+def calls_path() -> str:
+    """The file of _calls for this Python and this torch: it inlines structs of both, so another version of either
+    looks for, and builds, a file of its own."""
+    import torch
+    tag = f"{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}"
+    return os.path.join(PKG, f"_calls.{re.sub(r'[^A-Za-z0-9_.+-]', '_', tag)}.so")
+
+
+def _older(path: str, sources) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in sources)
+
+
+def library_stale() -> bool:
+    return _older(LIB, _sources() + _headers() + [__file__])
+
+
+def calls_stale() -> bool:
+    return _older(calls_path(), [_calls_source(), os.path.join(ROOT, "include", "bdattn.h"), __file__])
 
 
 def _run(cmd, what):
@@ -73,39 +86,37 @@ def _compile_calls() -> str:
 
 def _link_calls(obj: str):
     lib = os.path.join(list(importlib.util.find_spec("torch").submodule_search_locations)[0], "lib")
-    tmp = CALLS + f".tmp{os.getpid()}"
+    path = calls_path()
+    tmp = path + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libbdattn.so", f"-L{lib}", "-lc10", "-lc10_cuda",
-          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _calls.so")
-    os.replace(tmp, CALLS)
+          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _calls")
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale) and return the path of libbdattn.so."""
-    if not force and not _stale():
+    """Compile what is stale and return the path of libbdattn.so."""
+    library, calls = force or library_stale(), force or calls_stale()
+    if not library and not calls:
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
 
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc, *ARCH, *FLAGS, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        out = _run([nvcc, *ARCH, *FLAGS, "-c", src, "-o", obj], f"nvcc for {src}")
         if verbose:
-            sys.stdout.write(r.stdout + r.stderr)
+            sys.stdout.write(out)
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        calls = ex.submit(_compile_calls)
-        objs = list(ex.map(compile_one, _sources()))
-        calls = calls.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_calls(calls)
+        calls_obj = ex.submit(_compile_calls) if calls else None
+        if library:
+            objs = list(ex.map(compile_one, _sources()))
+            tmp = LIB + f".tmp{os.getpid()}"
+            _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], "link of libbdattn.so")
+            os.replace(tmp, LIB)
+        if calls:
+            _link_calls(calls_obj.result())
     return LIB
 
 

@@ -56,3 +56,31 @@ for call in (bdattn.bd_attn_paged4_decode, bdattn.bd_attn_paged_decode):
 def test_with_them(built, tmp_path):
     r = python(package_in(tmp_path, lambda name: False), "bdattn.load()\nassert bdattn._calls is not None")
     assert r.returncode == 0 and "Warning" not in r.stderr, r.stderr
+
+
+def test_the_module_is_of_one_torch_and_python(built, monkeypatch):
+    """It inlines torch's and Python's structs, so another version of either has a module of its own to build."""
+    import sysconfig
+
+    import torch
+    here = build.calls_path()
+    assert os.path.exists(here) and not build.calls_stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "9.9.9+cu990")
+        assert build.calls_path() != here and build.calls_stale() and not build.library_stale()
+    soabi = sysconfig.get_config_var("SOABI")
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-other" if name == "SOABI" else None)
+        assert soabi and build.calls_path() != here and build.calls_stale() and not build.library_stale()
+    assert build.calls_path() == here and not build.calls_stale()
+
+
+def test_a_module_of_another_torch_is_not_loaded(built, tmp_path):
+    """All files are there, under another torch: its module is not."""
+    r = python(package_in(tmp_path, lambda name: False), """
+import torch
+torch.__version__ = "9.9.9+cu990"
+bdattn.load()
+assert bdattn._calls is None
+""")
+    assert r.returncode == 0 and "RuntimeWarning" in r.stderr, r.stderr
