@@ -73,14 +73,33 @@ def _run(cmd, what):
     return r.stdout + r.stderr
 
 
-def _compile_calls() -> str:
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+def _calls_includes():
+    """The folders of the headers that _calls is compiled against, each behind the name of one of its files; none
+    where torch is not installed."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return []
+    torch = os.path.join(list(spec.submodule_search_locations)[0], "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    return [("bdattn.h", os.path.join(ROOT, "include")), ("Python.h", sysconfig.get_paths()["include"]),
+            ("cuda_runtime.h", cuda), ("ATen/core/Tensor.h", torch),
+            ("torch/all.h", os.path.join(torch, "torch", "csrc", "api", "include"))]
+
+
+def calls_lack() -> str:
+    """What _calls needs and is not here, or an empty text. The library needs none of it."""
+    if shutil.which("g++") is None:
+        return "g++"
+    includes = _calls_includes()
+    if not includes:
+        return "torch"
+    return ", ".join(os.path.join(d, f) for f, d in includes if not os.path.isfile(os.path.join(d, f)))
+
+
+def _compile_calls() -> str:
     obj = os.path.join(BUILD_DIR, "calls.o")
-    inc = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
-           os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{p}" for p in inc), "-c", _calls_source(),
-          "-o", obj], "g++ for calls.cpp")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{d}" for _, d in _calls_includes()), "-c",
+          _calls_source(), "-o", obj], "g++ for calls.cpp")
     return obj
 
 
@@ -94,8 +113,12 @@ def _link_calls(obj: str):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile what is stale and return the path of libbdattn.so."""
-    library, calls = force or library_stale(), force or calls_stale()
+    """Compile what is stale and return the path of libbdattn.so. _calls is left out, with a note, where what it alone
+    needs is not installed."""
+    lack = calls_lack()
+    library, calls = force or library_stale(), not lack and (force or calls_stale())
+    if lack and (lack == "torch" or force or calls_stale()):
+        print(f"_calls is left out: {lack} not found", file=sys.stderr)
     if not library and not calls:
         return LIB
     nvcc = _nvcc()

@@ -1,5 +1,6 @@
 """The binding's native part is an addition: without it every operator still runs, through Python and the C ABI."""
 import os
+import shutil
 import subprocess
 import sys
 
@@ -84,3 +85,54 @@ bdattn.load()
 assert bdattn._calls is None
 """)
     assert r.returncode == 0 and "RuntimeWarning" in r.stderr, r.stderr
+
+
+@pytest.mark.parametrize("missing", ["torch", "torch_headers", "Python.h", "g++"])
+def test_the_library_is_built_without_what_the_module_needs(built, monkeypatch, capsys, missing):
+    """Of the C ABI's library nothing needs torch, Python's headers or g++: it is brought up to date, and the module
+    that does is named as left out."""
+    import importlib.util
+    import sysconfig
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    old = os.path.getmtime(build.LIB)
+    ran = []
+
+    def run(cmd, what):  # the compiler's and linker's calls, of the library only
+        ran.append(what)
+        assert "calls" not in what
+        if "-shared" in cmd:
+            shutil.copy2(build.LIB, cmd[cmd.index("-o") + 1])
+        return ""
+
+    monkeypatch.setattr(build, "_run", run)
+    isfile, which, find = os.path.isfile, shutil.which, importlib.util.find_spec
+    if missing == "torch":
+        monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    elif missing == "torch_headers":
+        monkeypatch.setattr(os.path, "isfile", lambda p: not str(p).startswith(torch_dir) and isfile(p))
+    elif missing == "Python.h":
+        inc = sysconfig.get_paths()["include"]
+        monkeypatch.setattr(os.path, "isfile", lambda p: not str(p).startswith(inc) and isfile(p))
+    else:
+        monkeypatch.setattr(shutil, "which", lambda name, *a, **k: None if name == "g++" else which(name, *a, **k))
+    assert build.build(force=True) == build.LIB
+    assert "link of libbdattn.so" in ran and os.path.getmtime(build.LIB) == old
+    assert "_calls is left out" in capsys.readouterr().err
+
+
+def test_a_module_that_does_not_compile_is_an_error_behind_the_library(built, monkeypatch):
+    """Where everything is there but g++ fails, the library is in place before that is raised."""
+    ran = []
+
+    def run(cmd, what):
+        ran.append(what)
+        if "calls" in what:
+            raise RuntimeError(f"{what} failed")
+        if "-shared" in cmd:
+            shutil.copy2(build.LIB, cmd[cmd.index("-o") + 1])
+        return ""
+
+    monkeypatch.setattr(build, "_run", run)
+    with pytest.raises(RuntimeError, match="calls"):
+        build.build(force=True)
+    assert "link of libbdattn.so" in ran
