@@ -87,7 +87,7 @@ def _calls_includes():
 
 
 def calls_lack() -> str:
-    """What _calls needs and is not here, or an empty text. The library needs none of it."""
+    """What _calls needs to be built and is not here, or an empty text. The library needs none of it."""
     if shutil.which("g++") is None:
         return "g++"
     includes = _calls_includes()
@@ -115,10 +115,11 @@ def _link_calls(obj: str):
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile what is stale and return the path of libbdattn.so. _calls is left out, with a note, where what it alone
     needs is not installed."""
-    lack = calls_lack()
-    library, calls = force or library_stale(), not lack and (force or calls_stale())
-    if lack and (lack == "torch" or force or calls_stale()):
+    library = force or library_stale()
+    calls = importlib.util.find_spec("torch") is None or force or calls_stale()
+    if calls and (lack := calls_lack()):
         print(f"_calls is left out: {lack} not found", file=sys.stderr)
+        calls = False
     if not library and not calls:
         return LIB
     nvcc = _nvcc()

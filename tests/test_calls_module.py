@@ -136,3 +136,9 @@ def test_a_module_that_does_not_compile_is_an_error_behind_the_library(built, mo
     with pytest.raises(RuntimeError, match="calls"):
         build.build(force=True)
     assert "link of libbdattn.so" in ran
+
+
+def test_what_is_up_to_date_needs_no_compiler(built, monkeypatch, capsys):
+    monkeypatch.setattr(shutil, "which", lambda *a, **k: None)
+    monkeypatch.setattr(build, "_nvcc", lambda: 1 / 0)
+    assert build.build() == build.LIB and capsys.readouterr().err == ""
