@@ -138,7 +138,9 @@ def test_a_module_that_does_not_compile_is_an_error_behind_the_library(built, mo
     assert "link of libbdattn.so" in ran
 
 
-def test_what_is_up_to_date_needs_no_compiler(built, monkeypatch, capsys):
-    monkeypatch.setattr(shutil, "which", lambda *a, **k: None)
+@pytest.mark.parametrize("gxx", [True, False])
+def test_what_is_up_to_date_needs_no_compiler(built, monkeypatch, capsys, gxx):
     monkeypatch.setattr(build, "_nvcc", lambda: 1 / 0)
+    if not gxx:
+        monkeypatch.setattr(shutil, "which", lambda *a, **k: None)
     assert build.build() == build.LIB and capsys.readouterr().err == ""
