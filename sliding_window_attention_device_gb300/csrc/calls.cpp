@@ -5,7 +5,8 @@
 // they are as they should be (types, shapes, places, the current device), allocates
 // what was not given, and calls the C ABI on the current stream. Where something is not
 // as it should be it does nothing and returns None, and bdattn.py goes on to say what:
-// it holds the same checks in full, and the same call.
+// it holds the same checks in full, and the same call. Outputs are allocated and the
+// kernels launched without the interpreter's lock, as both may wait for the GPU.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
@@ -99,24 +100,31 @@ PyObject* failed(int rc, const char* what) {
 bool given(const Call& c, PyObject* o, at::ScalarType type, at::IntArrayRef shape) {
   return o == Py_None || c.is(o, type, shape);
 }
-// `o` once more, or a tensor made now
-PyObject* made(const Call& c, PyObject* o, at::ScalarType type, at::IntArrayRef shape) {
-  if (o != Py_None) {
-    Py_INCREF(o);
-    return o;
-  }
-  return THPVariable_Wrap(c.make(shape, type));
-}
+// An output: the one given, or one made here.
+struct Out {
+  PyObject* o;
+  at::Tensor made;
+  void* at = nullptr;
 
-struct Ref {  // a reference that ends here unless it is handed on
+  explicit Out(PyObject* given) : o(given), at(given != Py_None ? data(given) : nullptr) {}
+  // without the lock
+  void make(const Call& c, at::ScalarType type, at::IntArrayRef shape) {
+    if (o != Py_None) return;
+    made = c.make(shape, type);
+    at = made.data_ptr();
+  }
+  PyObject* give() const { return o != Py_None ? Py_NewRef(o) : THPVariable_Wrap(made); }
+};
+
+struct Unlocked {  // the interpreter's lock is free while one of these lives
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+struct Ref {  // a reference that ends here
   PyObject* o;
   explicit Ref(PyObject* x) : o(x) {}
   ~Ref() { Py_XDECREF(o); }
-  PyObject* give() {
-    PyObject* x = o;
-    o = nullptr;
-    return x;
-  }
 };
 
 // (q_new, k_new, v_new, cos_sin, cu_new, seq_lens, page_table, pg, cache or (k_pages, v_pages), status, pairing,
@@ -159,27 +167,33 @@ PyObject* append(PyObject* const* a, bool four) {
     r.rot_dim = static_cast<int>(t.size(1));
     angles = data_of<const float>(cs);
   }
-  Ref to(nullptr);
+  const void* q_at = nullptr;
   if (q != Py_None) {
     if (!c.rows(q, T, Hq, &r.q_stride) || !given(c, q_out, at::kBFloat16, {T, Hq, D})) Py_RETURN_NONE;
-    to.o = made(c, q_out, at::kBFloat16, {T, Hq, D});
-    if (to.o == nullptr) return nullptr;
+    q_at = data(q);
   } else if (q_out != Py_None) {
     Py_RETURN_NONE;
   }
-  const void* q_at = q != Py_None ? data(q) : nullptr;
-  void *q_to = to.o != nullptr ? data(to.o) : nullptr, *k_to = k_out != Py_None ? data(k_out) : nullptr;
+  Out to(q_out);
+  const void *k_at = data(k), *v_at = data(v);
+  void* k_to = k_out != Py_None ? data(k_out) : nullptr;
   const int n = static_cast<int>(T);
   const int32_t *cu_at = data_of<const int32_t>(cu), *lens_at = data_of<const int32_t>(lens),
                 *table_at = data_of<const int32_t>(table);
-  const int rc = four ? bd_attn_paged4_append(q_at, data(k), data(v), angles, &r, cu_at, lens_at, table_at, &c.g, n,
-                                              q_to, k_to, &cache, data_of<int32_t>(status), c.stream())
-                      : bd_attn_paged_append_rope(q_at, data(k), data(v), angles, &r, cu_at, lens_at, table_at, &c.g, n,
-                                                  q_to, k_to, kp, vp, data_of<int32_t>(status), c.stream());
+  int32_t* status_at = data_of<int32_t>(status);
+  int rc;
+  {
+    const Unlocked unlocked;
+    if (q != Py_None) to.make(c, at::kBFloat16, {T, Hq, D});
+    rc = four ? bd_attn_paged4_append(q_at, k_at, v_at, angles, &r, cu_at, lens_at, table_at, &c.g, n, to.at, k_to,
+                                      &cache, status_at, c.stream())
+              : bd_attn_paged_append_rope(q_at, k_at, v_at, angles, &r, cu_at, lens_at, table_at, &c.g, n, to.at, k_to,
+                                          kp, vp, status_at, c.stream());
+  }
   if (rc != BD_OK) return failed(rc, four ? "bd_attn_paged4_append" : "bd_attn_paged_append_rope");
   // a tuple, as None means that nothing was done
-  Ref result(to.o != nullptr ? to.give() : Py_NewRef(Py_None));
-  return PyTuple_Pack(1, result.o);
+  const Ref result(q != Py_None ? to.give() : Py_NewRef(Py_None));
+  return result.o != nullptr ? PyTuple_Pack(1, result.o) : nullptr;
 }
 
 PyObject* append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -196,6 +210,11 @@ PyObject* append4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+PyObject* both(const Out& x, const Out& y) {
+  const Ref a(x.give()), b(y.give());
+  return a.o != nullptr && b.o != nullptr ? PyTuple_Pack(2, a.o, b.o) : nullptr;
+}
+
 // (cache, cu, seq_lens, page_table, pg, n_tokens, status, k_out, v_out) -> (k_out, v_out)
 PyObject* read4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -210,13 +229,20 @@ PyObject* read4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const int64_t shape[3] = {T, c.g.Hkv, c.g.D};
   if (!given(c, a[7], at::kBFloat16, shape) || !given(c, a[8], at::kBFloat16, shape)) Py_RETURN_NONE;
-  Ref k(made(c, a[7], at::kBFloat16, shape)), v(made(c, a[8], at::kBFloat16, shape));
-  if (k.o == nullptr || v.o == nullptr) return nullptr;
-  const int rc = bd_attn_paged4_read(&cache, data_of<const int32_t>(a[1]), data_of<const int32_t>(a[2]),
-                                     data_of<const int32_t>(a[3]), &c.g, static_cast<int>(T), data(k.o), data(v.o),
-                                     data_of<int32_t>(a[6]), c.stream());
+  const int32_t *cu_at = data_of<const int32_t>(a[1]), *lens_at = data_of<const int32_t>(a[2]),
+                *table_at = data_of<const int32_t>(a[3]);
+  int32_t* status_at = data_of<int32_t>(a[6]);
+  Out k(a[7]), v(a[8]);
+  int rc;
+  {
+    const Unlocked unlocked;
+    k.make(c, at::kBFloat16, shape);
+    v.make(c, at::kBFloat16, shape);
+    rc = bd_attn_paged4_read(&cache, cu_at, lens_at, table_at, &c.g, static_cast<int>(T), k.at, v.at, status_at,
+                             c.stream());
+  }
   if (rc != BD_OK) return failed(rc, "bd_attn_paged4_read");
-  return PyTuple_Pack(2, k.o, v.o);
+  return both(k, v);
   END_HANDLE_TH_ERRORS
 }
 
@@ -233,21 +259,21 @@ PyObject* decode4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const int64_t bytes = static_cast<int64_t>(bd_attn_paged4_decode_workspace_bytes(&c.g));
   if (bytes == 0 || !given(c, a[8], at::kByte, {bytes})) Py_RETURN_NONE;
-  Ref out(made(c, a[6], at::kBFloat16, {B, Hq, D})), lse(made(c, a[7], at::kFloat, {B, Hq}));
-  if (out.o == nullptr || lse.o == nullptr) return nullptr;
-  at::Tensor ours;
-  void* workspace = nullptr;
-  if (a[8] != Py_None) {
-    workspace = data(a[8]);
-  } else if (bytes > 16) {  // 16: the call needs none
-    ours = c.make({bytes}, at::kByte);
-    workspace = ours.data_ptr();
+  const void* q_at = data(a[0]);
+  const int32_t *table_at = data_of<const int32_t>(a[2]), *lens_at = data_of<const int32_t>(a[3]);
+  int32_t* status_at = data_of<int32_t>(a[5]);
+  Out out(a[6]), lse(a[7]), workspace(a[8]);
+  int rc;
+  {
+    const Unlocked unlocked;
+    out.make(c, at::kBFloat16, {B, Hq, D});
+    lse.make(c, at::kFloat, {B, Hq});
+    if (bytes > 16) workspace.make(c, at::kByte, {bytes});  // 16: the call needs none
+    rc = bd_attn_paged4_decode(q_at, &cache, table_at, lens_at, &c.g, out.at, static_cast<float*>(lse.at),
+                               workspace.at, status_at, c.stream());
   }
-  const int rc = bd_attn_paged4_decode(data(a[0]), &cache, data_of<const int32_t>(a[2]), data_of<const int32_t>(a[3]),
-                                       &c.g, data(out.o), data_of<float>(lse.o), workspace, data_of<int32_t>(a[5]),
-                                       c.stream());
   if (rc != BD_OK) return failed(rc, "bd_attn_paged4_decode");
-  return PyTuple_Pack(2, out.o, lse.o);
+  return both(out, lse);
   END_HANDLE_TH_ERRORS
 }
 
