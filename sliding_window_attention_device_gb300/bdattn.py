@@ -842,6 +842,11 @@ def _token_rows(t, name, i: int, T: int, heads: int, D: int) -> int:
     raise ValueError(f"{name}: {what}, expected bfloat16 [{T}, {heads}, {D}] on cuda:{i}")
 
 
+def _rope(rot, pairing, n_pos, q_stride, k_stride, v_stride) -> Rope:
+    _fit(Rope, (rot, pairing, n_pos))
+    return Rope(rot, pairing, n_pos, q_stride, k_stride, v_stride)
+
+
 def _append_rope(fn, q_new, k_new, v_new, cos_sin, cu_new, seq_lens, page_table, pg: Paged, status, pairing, q_out,
                  k_out, dev, i, T, B, Hkv, D, cache):
     k_stride, v_stride = _token_rows(k_new, "k_new", i, T, Hkv, D), _token_rows(v_new, "v_new", i, T, Hkv, D)
@@ -873,7 +878,7 @@ def _append_rope(fn, q_new, k_new, v_new, cos_sin, cu_new, seq_lens, page_table,
     if not _places_ok(i, cu_new, seq_lens, page_table, status, B, pg.max_pages):
         _want(dev, (cu_new, "cu_new", _I32, (B + 1,)), (seq_lens, "seq_lens", _I32, (B,)),
               (page_table, "page_table", _I32, (B, pg.max_pages)), (status, "status", _I32, (1,)))
-    rc = fn(q_at, k_new.data_ptr(), v_new.data_ptr(), angles, Rope(rot, pairing, n_pos, q_stride, k_stride, v_stride),
+    rc = fn(q_at, k_new.data_ptr(), v_new.data_ptr(), angles, _rope(rot, pairing, n_pos, q_stride, k_stride, v_stride),
             cu_new.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), pg, T, q_to, k_to, *cache,
             status.data_ptr(), _current(dev))
     if rc:

@@ -40,3 +40,11 @@ def test_sinks():
     assert bdattn.paged_geom(**PAGED, window=3, n_sink=2 ** 40).n_sink == 2 ** 31 - 1  # all of them
     with pytest.raises(ValueError, match="n_sink"):
         bdattn.paged_geom(**PAGED, n_sink=-2 ** 40)
+
+
+@pytest.mark.parametrize("name,values", [("pairing", (64, 2 ** 32, 100)), ("pairing", (64, -2 ** 32 + 1, 100)),
+                                         ("n_pos", (0, 0, 2 ** 32 + 5))])
+def test_rope(name, values):
+    with pytest.raises(ValueError, match=name):
+        bdattn._rope(*values, 0, 0, 0)
+    assert bdattn._rope(64, 1, 100, 512, 256, 2 ** 31).v_stride == 2 ** 31
