@@ -87,10 +87,13 @@ __host__ __device__ inline bool dec_whole_rows(const PagedGeom& g) {
   return n <= 512 || (n <= 2048 && rows >= 128);
 }
 // The same over 4-bit pages, whose steps cost a CTA by their bytes: keys count D / 128
-// times from D 128 on. In us, whole and cut: 8 rows of 608 keys at D 128 6.2 and 7.9, of
-// 1,024 8.0 and 8.0; at D 256 9.9 and 8.6, 14.3 and 8.7; at D 512 256 keys 8.3 and 10.7.
-// 128 rows of 2,048 at D 128 13.9 and 19.0 (ragged 13.5 and 16.2), of 4,096 23.5 and 25.3
-// (22.8 and 18.6); of 1,024 at D 256 15.4 and 19.2 (14.6 and 16.2).
+// times from D 128 on. In us, whole and cut: 8 rows of 608 keys at D 128 6.4 and 8.4, of
+// 1,024 8.0 and 8.4; at D 256 9.9 and 9.1, 13.9 and 9.3; at D 512 256 keys 8.8 and 10.7.
+// 128 rows of 2,048 at D 128 14.4 and 19.4 (ragged 14.0 and 16.4), of 4,096 24.2 and 26.1
+// (23.6 and 19.0); of 1,024 at D 256 15.1 and 19.7 (14.5 and 16.5). The limit is one for
+// ragged rows. Rows that a window shorter than all sequences makes equally long would be
+// faster whole beyond it: 128 rows at D 128 with a window of 2,560 17.4 and 21.4, of 4,096
+// 25.0 and 26.3, at D 256 of 1,280 18.4 and 20.9, of 2,048 26.8 and 26.8.
 __host__ __device__ constexpr int dec4_ctas(int D, int nt) {
   return D * nt <= 128 || (D == 256 && nt == 1) ? 2 * kSms : kSms;
 }

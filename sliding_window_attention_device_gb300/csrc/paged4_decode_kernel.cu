@@ -24,20 +24,20 @@
 // transposing load, no shuffle; 16-byte pieces are swizzled so that the loads touch every
 // bank as often.
 //   A step is 32 keys of a warp (16 from D 256 on), beginning at a multiple of that; a
-// step whose keys are all visible needs no masks, and where pages are multiples of 16
-// tokens its 16-key halves are pieces of the cache, one address each (one per row
-// elsewhere: pages of 200 at D 128 45 us for 43.5).
+// step of the window whose keys are all visible needs no masks, and where pages are
+// multiples of 16 tokens its 16-key halves are pieces of the cache, one address each (one
+// per row elsewhere: pages of 200 at D 128 50 us for 48). The sinks' steps are masked ones
+// also where they are whole: meant for a few of them.
 //   The line of all rows' steps is cut for each row by itself where rows are few, into
 // equal pieces otherwise, with a charge for each row's start (kRowStart): a CTA that
 // goes from one row to the next waits for a page number, for keys and for its warps.
 //
 // What bounds it. 16 keys of D 128 are 2,304 bytes, 392 clocks of an SM's quarter at the
-// copy rate, and some 320 instructions (304 measured with one number per weight: 64
-// conversions, 64 products with scales, 16 mma, 12 loads from shared memory, the rest
-// copies, softmax and addresses; the second one adds 8 mma and a dozen more). Without any
-// copies that took 327 clocks, and 8 mma are some 65: conversions, half-precision
-// products and mma.sync hardly overlap on the SM. So instructions bound it, bytes close
-// behind. 16 ragged sequences to 32,768 keys, 8 kv heads of 8 heads each, D 128, 312 MB:
+// copy rate, and 325 instructions (measured; 64 conversions, 64 products with scales, 24
+// mma, 12 loads from shared memory, the rest copies, softmax and addresses). With one
+// number per weight, 16 mma and no copies the work took 327 clocks, and 8 mma more are
+// some 65: conversions, half-precision products and mma.sync hardly overlap on the SM. So
+// instructions and bytes bound it about alike. 16 ragged sequences to 32,768 keys, 8 kv heads of 8 heads each, D 128, 312 MB:
 // 75 us, 4.2 TB/s (the bf16 pages of the same keys: 172 us); D 64, 156 MB 50 us; D 256,
 // 313 MB 76; D 512 68. With 16 heads each D 64 72, D 128 110, D 256 109. A call with few
 // steps is 3 us of a launch, page number, keys and softmax, one after the other, and 2 to
@@ -62,7 +62,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSpan = 8;  // sequences of a lane where a warp sums up all of them
 // What a row's start in a CTA's midst costs, in steps (312 MB over 128 rows with 0, 12,
-// 24 and 48: 72.2, 67.8, 67.3 and 69.5 us; head dim 512: 74.2, 66.9, 64.9 and 66.8).
+// 24 and 48: 77.7, 74.7, 74.9 and 77.4 us; head dim 512: 78.7, 70.6, 67.9 and 69.9).
 constexpr int kRowStart = 24;
 // How the line is cut: a row per CTA; or equal pieces, rows that are cut being named by
 // the CTA they start in, or, where there are no more rows than CTAs, by their number.
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     }
 
     // ---- this warp's steps: t0 + warp, t0 + warp + kWarps, ...
-    // Steps [full0, full0 + n_full) see all of their keys.
+    // Steps [full0, full0 + n_full), of the window, see all of their keys.
     constexpr int kStep = C::kStep;
     const int full0 = sq.sinks + (sq.lo % kStep != 0);
     const int n_full = max(steps - (sq.len % kStep != 0) - full0, 0);
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
             cp_async_all<16>(dst + C::kKBlocks + lane * 16, c4.k_blocks + block);
             cp_async_all<16>(dst + C::kVBlocks + lane * 16, c4.v_blocks + block);
           }
-        } else {  // the first and last steps: zeros for keys that are not to be seen
+        } else {  // the sinks' steps, the window's first and last: zeros for keys that are not to be seen
           const int base = sq.base(t);
           const bool seen = key >= sq.a(t, base) && key < sq.e(t, base);
           if (seen && !in_cache) atomicOr(status, BD_STATUS_BOUNDS);

@@ -10,8 +10,9 @@
 // Bytes bound the large calls: everything is read and written once, whole sectors by
 // neighbouring threads. In front of them is a chain of small loads (offsets, length, page)
 // that finds where a token goes: one warp per CTA runs it, 32 offsets a trip, while the
-// CTA's first pieces of q, k and v are already on their way, and a CTA takes as many
-// tokens as let all CTAs be there at once. 13,800 tokens of 32 + 2 x 8 heads, D 128, 340 MB:
+// CTA's first pieces of q, k and v are already on their way, and a CTA takes up to 32
+// tokens: into bf16 pages as many as let all CTAs be on the SMs at once, up to 38,912
+// tokens; the others below are several waves. 13,800 tokens of 32 + 2 x 8 heads, D 128, 340 MB:
 // 57 us, 5.9 TB/s (of a plain copy's 6.6 in the same run); without the rotation 55. 64
 // single tokens 3.5 us, 3 of them that chain and a launch. Threads in flight count for more
 // than loads of a thread: two heads at a time at 64 registers 58 us, three at 80 64.
@@ -20,8 +21,8 @@
 // for 292 MB. They have CTAs of their own, in front (among those of the queries 57 to 61,
 // the queries in the same CTAs 70).
 //   Reading back is bound by the rows written: 55,700 tokens, 8 heads, 292 MB 48 us, 6.1
-// TB/s; 16 numbers a thread, in two stores 32 bytes apart, 63; 16 CTAs' worth of tokens
-// per SM at once instead of 64 58, as few waves end unevenly.
+// TB/s; 16 numbers a thread, in two stores 32 bytes apart, 63; 16 CTAs per SM, one wave,
+// instead of 64 of fewer tokens 58, as few waves end unevenly.
 #include <cuda_bf16.h>
 #include <cstdint>
 
@@ -33,7 +34,7 @@ namespace bd {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeCtas = 8;   // per SM
+constexpr int kRopeCtas = 8;   // of the append, on an SM at once
 constexpr int kRopeTok = 32;   // tokens of a CTA at most
 constexpr int kReadBatch = 2;  // pieces that a thread has in flight
 
@@ -431,8 +432,10 @@ __global__ void __launch_bounds__(kRopeThreads)
 }
 
 // Tokens a CTA takes, of `items` items each: enough for its threads; and where there are
-// more, all that is there at once, `share` of kRopeCtas CTAs per SM (finding the tokens'
-// places is then paid once).
+// more, so many that `share` CTAs per SM are launched, as finding the tokens' places is
+// paid per CTA; kRopeTok at most. The append into bf16 pages asks for the 8 that an SM
+// holds; the one into 4 bits for 8 of keys and values and 16 of queries, and the read for
+// 64, which run in several waves.
 int tokens_per_cta(int n_tokens, int items, int share) {
   const int least = (kRopeThreads + items - 1) / items, ctas = kSms * share;
   int tok = (n_tokens - 1) / ctas + 1;
