@@ -41,6 +41,8 @@ def test_other_threads_run_while_a_call_waits(what):
     assert bdattn._calls is not None
     torch.cuda.synchronize()
     # cycles of a second: counted on this GPU
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
     a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     a.record()
     torch.cuda._sleep(10_000_000)
