@@ -13,9 +13,10 @@
 // what the first left, off by 2^-22 of it or by 2^-32 of the largest: out is then off by
 // its own rounding only. The second one costs a second product with V, but where a row
 // has at most 4 heads (kFold): they stand twice among a product's 8 columns, which hold
-// first parts in one half and second parts in the other. Two products: 16 sequences to
-// 32,768 keys at 8 heads 75 us (one number per weight: 67), at 16 heads 110 (92); folded:
-// 32 sequences with a window of 1024 at D 256 and 2 heads 22.5 (22.1).
+// first parts in one half and second parts in the other. 16 sequences to 32,768 keys with 4
+// heads 66.7 us folded, 72.8 with two products (D 64 44.9 and 47.5); 32 with a window of
+// 1024 at D 256 and 2 heads 22.4 and 24.0. One number per weight took 67 us for 8 heads
+// (two: 75) and 92 for 16 (110).
 //   The order of d within a product and of keys within a step is free as long as both
 // factors share it. So lane (g, c) = (lane / 4, lane % 4) of the K product reads a
 // quarter of a key's row, D / 8 bytes, from shared memory at once and makes its part of
@@ -37,13 +38,15 @@
 // mma, 12 loads from shared memory, the rest copies, softmax and addresses). With one
 // number per weight, 16 mma and no copies the work took 327 clocks, and 8 mma more are
 // some 65: conversions, half-precision products and mma.sync hardly overlap on the SM. So
-// instructions and bytes bound it about alike. 16 ragged sequences to 32,768 keys, 8 kv heads of 8 heads each, D 128, 312 MB:
-// 75 us, 4.2 TB/s (the bf16 pages of the same keys: 172 us); D 64, 156 MB 50 us; D 256,
-// 313 MB 76; D 512 68. With 16 heads each D 64 72, D 128 110, D 256 109. A call with few
-// steps is 3 us of a launch, page number, keys and softmax, one after the other, and 2 to
-// 3 of the join: one sequence of 1,000 keys 8 us, of 131,072 (75 MB) 26.
-//   Tried and not kept, for the 312 MB, all with one number per weight: bulk copies by one lane 79 us for 67 (many small
-// ones); K and V as items of their own 77 for 74; 24 warps an SM at 80 registers 105;
+// instructions and bytes bound it about alike. 16 ragged sequences to 32,768 keys, 8 kv
+// heads of 8 heads each, D 128, 312 MB: 75 us, 4.2 TB/s (the bf16 pages of the same keys:
+// 172 us); D 64, 156 MB 50 us; D 256, 313 MB 76; D 512 68. With 16 heads each D 64 72,
+// D 128 110, D 256 109. A call with few steps is 3 us of a launch, page number, keys and
+// softmax, one after the other, and 2 to 3 of the join: one sequence of 1,000 keys 8 us,
+// of 131,072 (75 MB) 26.
+//   Tried and not kept, for the 312 MB, all with one number per weight: bulk copies by
+// one lane 79 us for 67 (many small ones); K and V as items of their own 77 for 74; 24
+// warps an SM at 80 registers 105;
 // every warp with a piece of the line of its own 69 for 72, but 28 for 22 at 1,028 keys
 // of D 256. Two CTAs an SM, but for 16 heads at D 128 (91 us with one and 236 registers,
 // 113 with two) and D 256, and for D 512.
